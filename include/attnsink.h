@@ -53,7 +53,8 @@ enum attn_dtype {
     ATTN_DTYPE_BF16 = 1,
     ATTN_DTYPE_F32 = 2,
     ATTN_DTYPE_I32 = 3,
-    ATTN_DTYPE_E4M3 = 4   /* FP8: 1 sign, 4 exponent (bias 7), 3 mantissa bits */
+    ATTN_DTYPE_E4M3 = 4,  /* FP8: 1 sign, 4 exponent (bias 7), 3 mantissa bits */
+    ATTN_DTYPE_E8M0 = 5   /* a power of two: byte b stands for 2^(b-127), 255 for NaN */
 };
 
 typedef struct attn_tensor {
@@ -315,6 +316,101 @@ int attn_sink_decode_noalloc(const attn_tensor *q, const attn_tensor *kcache,
                              const attn_tensor *vcache, const attn_tensor *seqlens,
                              const attn_tensor *sinks, int32_t window, float scale,
                              attn_tensor *out, void *stream);
+
+/*
+ * The 8-bit paged cache (page "Dao-AILab/flash-attention" contributor guide:
+ * paged KV; page "cf-1.com/news/6055759", "fix 2": an FP8 cache with its
+ * descales).  Its tensors, shared by the three calls below:
+ *
+ *   kpages, vpages    [NB, P, Hkv, D] ATTN_DTYPE_E4M3 codes: NB >= 1 physical
+ *                     pages of P positions, P a power of two in [16, 65536],
+ *                     D in {64, 128, 256}.
+ *   kscales, vscales  [NB, Hkv, P]    ATTN_DTYPE_E8M0: a power-of-two scale for
+ *                     every position and kv head: row = scale * codes.
+ *                     (Of all four, every stride but the innermost is a
+ *                     multiple of 16 elements.)
+ *   block_table       [B, MP] int32, DEVICE memory (innermost stride 1):
+ *                     position t of sequence b is row t % P of page
+ *                     block_table[b][t / P].  Pages may be shared between
+ *                     sequences.
+ *   seqlens           [B] int32, DEVICE memory: cached positions of each
+ *                     sequence, clamped to [0, MP * P].
+ *
+ * The same tensors go to each call, so that append then decode needs no other
+ * bookkeeping than the lengths.  B <= 2^20, MP * P <= 2^30, Hkv <= 65535.
+ */
+
+/*
+ * Write: quantises new key and value rows as they enter the cache.
+ *
+ *   k, v        [T, Hkv, D] bf16, the new rows of all sequences, packed
+ *   cu_seqlens  [B + 1] int32, DEVICE memory, non-decreasing: rows
+ *               cu_seqlens[b] .. cu_seqlens[b+1]-1 belong to sequence b and
+ *               become its LAST positions, i.e. row r goes to position
+ *               seqlens[b] - (cu_seqlens[b+1] - r): seqlens already counts
+ *               them, as attn_sink_decode_paged_fp8 wants it.
+ *
+ * Each row's scale is 2^e with e the smallest integer in [-117, 119] such that
+ * max|x| <= 448 * 2^e; its codes are x / 2^e rounded to nearest even: an error
+ * of at most 2^-4 |x| (2^-10 * 2^e for |x| < 2^-6 * 2^e).  NaN and infinities
+ * become the NaN code 0x7F and do not enter the maximum; a magnitude above 448 * 2^119
+ * saturates.  Only the T rows' places are written.  A row whose position is
+ * negative, or whose page is outside the table or the pool, is dropped, and so
+ * are rows outside [cu_seqlens[0], cu_seqlens[B]).  Two rows of one call must
+ * not have the same place (sequences that share a page do not write to it):
+ * the place would hold parts of both.
+ * One launch, no workspace.  T = 0 or B = 0 is a no-op.
+ */
+int attn_sink_cache_append_fp8(const attn_tensor *k, const attn_tensor *v, const attn_tensor *block_table,
+                               const attn_tensor *seqlens, const attn_tensor *cu_seqlens,
+                               attn_tensor *kpages, attn_tensor *vpages, attn_tensor *kscales,
+                               attn_tensor *vscales, void *stream);
+
+/*
+ * Read back: the last rows of every sequence as packed bf16, for example the
+ * keys a prompt chunk continues from (attn_sink_fwd_extend).
+ *
+ *   cu_seqlens  [B + 1] as above: row r of k and v is position
+ *               seqlens[b] - (cu_seqlens[b+1] - r) of its sequence.
+ *   k, v        [T, Hkv, D] bf16, written for the rows in [cu_seqlens[0],
+ *               cu_seqlens[B]); rows outside stay as they are.
+ *
+ * scale * code is exact in bf16 for everything the append writes (for other
+ * scale bytes: rounded to nearest even).  A row whose position is negative, or
+ * whose page is outside the table or the pool, reads as zeros.
+ * One launch, no workspace.  T = 0 or B = 0 is a no-op.
+ */
+int attn_sink_cache_read_fp8(const attn_tensor *kpages, const attn_tensor *vpages,
+                             const attn_tensor *kscales, const attn_tensor *vscales,
+                             const attn_tensor *block_table, const attn_tensor *seqlens,
+                             const attn_tensor *cu_seqlens, attn_tensor *k, attn_tensor *v, void *stream);
+
+/*
+ * Single-token decode over the 8-bit paged cache: attn_sink_decode_paged with
+ * key row = kscale * codes and value row = vscale * codes.
+ *
+ *   q, out         [B, Hq, D] bf16; the query of sequence b sits at position
+ *                  seqlens[b]-1, its own key and value already appended.
+ *   sinks, window, scale: as for attn_sink_decode.
+ * A sequence of length 0 yields a zero row.  Table entries of pages that hold
+ * no visible position may hold anything; an entry outside [0, NB) reads as a
+ * page of zero rows.  Cache rows outside the window may hold anything, NaN
+ * included.  A NaN scale or code of a visible row reaches the outputs of its
+ * kv head.  Hq/Hkv <= 16 (<= 8 at D = 256; larger groups return
+ * ATTN_EUNSUPPORTED).
+ *
+ * Two launches on `stream`, no host synchronisation: the split kernel divides
+ * the visible keys of the whole batch evenly over the SMs and finishes every
+ * sequence that was not cut; a combine kernel merges the cut ones.  The result
+ * does not depend on what else runs (no atomics).  Workspace, from the
+ * library's stream-ordered pool: at most about 2 * (SMs / Hkv + 1) * Hq *
+ * (D + 1) * 4 bytes, whatever the lengths.
+ */
+int attn_sink_decode_paged_fp8(const attn_tensor *q, const attn_tensor *kpages, const attn_tensor *vpages,
+                               const attn_tensor *kscales, const attn_tensor *vscales,
+                               const attn_tensor *block_table, const attn_tensor *seqlens,
+                               const attn_tensor *sinks, int32_t window, float scale, attn_tensor *out,
+                               void *stream);
 
 /*
  * Synchronises `stream`, then returns and clears the device status word of the

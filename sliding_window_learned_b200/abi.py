@@ -29,14 +29,17 @@ ATTN_DTYPE_BF16 = 1
 ATTN_DTYPE_F32 = 2
 ATTN_DTYPE_I32 = 3
 ATTN_DTYPE_E4M3 = 4
+ATTN_DTYPE_E8M0 = 5
 
 _DTYPES = {torch.bfloat16: ATTN_DTYPE_BF16, torch.float32: ATTN_DTYPE_F32,
-           torch.int32: ATTN_DTYPE_I32, torch.float8_e4m3fn: ATTN_DTYPE_E4M3}
+           torch.int32: ATTN_DTYPE_I32, torch.float8_e4m3fn: ATTN_DTYPE_E4M3,
+           torch.float8_e8m0fnu: ATTN_DTYPE_E8M0}
 
 # Every symbol include/attnsink.h declares.
 EXPORTS = ("attn_sink_fwd", "attn_sink_fwd_max_logit", "attn_sink_fwd_varlen", "attn_sink_bwd", "attn_sink_fwd_cudacore", "attn_sink_decode",
            "attn_sink_decode_chunked", "attn_sink_decode_paged", "attn_sink_decode_fp8",
            "attn_sink_decode_noalloc",
+           "attn_sink_cache_append_fp8", "attn_sink_cache_read_fp8", "attn_sink_decode_paged_fp8",
            "attn_sink_get_status", "attn_sink_set_wait_limit_ns", "attn_sink_fail_workspace_allocs",
            "attn_sink_strerror", "attn_sink_last_error")
 
@@ -86,6 +89,12 @@ def load() -> ctypes.CDLL:
         lib.attn_sink_decode_fp8.restype = ctypes.c_int
         lib.attn_sink_decode_noalloc.argtypes = [P, P, P, P, P, i32, f32, P, V]
         lib.attn_sink_decode_noalloc.restype = ctypes.c_int
+        for name in ("attn_sink_cache_append_fp8", "attn_sink_cache_read_fp8"):
+            fn = getattr(lib, name)
+            fn.argtypes = [P] * 9 + [V]
+            fn.restype = ctypes.c_int
+        lib.attn_sink_decode_paged_fp8.argtypes = [P] * 8 + [i32, f32, P, V]
+        lib.attn_sink_decode_paged_fp8.restype = ctypes.c_int
         lib.attn_sink_get_status.argtypes = [V]
         lib.attn_sink_get_status.restype = ctypes.c_int
         lib.attn_sink_set_wait_limit_ns.argtypes = [ctypes.c_uint64]
@@ -260,6 +269,55 @@ def attn_sink_decode_noalloc(q, kcache, vcache, seqlens, sinks, window: int, sca
                                       _ref(ds[4]), int(window), float(scale), _ref(ds[5]),
                                       _stream(stream, q))
     _check(rc, "attn_sink_decode_noalloc")
+
+
+def _on_device(where: str, tensors, call):
+    """Run ``call`` with the tensors' device current, after checking that all
+    of them (None aside) are on one CUDA device: the library reads the pointers
+    on the device and cannot check where they lead."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev or dev < 0:
+            raise ValueError(f"{where}: tensors must be on one CUDA device")
+    if dev == torch.cuda.current_device():
+        return call()
+    with torch.cuda.device(dev):
+        return call()
+
+
+def attn_sink_cache_append_fp8(k, v, block_table, seqlens, cu_seqlens, kpages, vpages, kscales,
+                               vscales, stream=None):
+    """C ``attn_sink_cache_append_fp8``: packed bf16 rows k, v ``[T, Hkv, D]``
+    quantised into the page pools kpages, vpages (``torch.float8_e4m3fn``
+    ``[NB, P, Hkv, D]``) and their scales kscales, vscales
+    (``torch.float8_e8m0fnu`` ``[NB, Hkv, P]``), as the last positions of each
+    sequence (``seqlens`` counts them already)."""
+    ts = (k, v, block_table, seqlens, cu_seqlens, kpages, vpages, kscales, vscales)
+    rc = _on_device("attn_sink_cache_append_fp8", ts, lambda: load().attn_sink_cache_append_fp8(
+        *[_ref(describe(t)) for t in ts], _stream(stream, k)))
+    _check(rc, "attn_sink_cache_append_fp8")
+
+
+def attn_sink_cache_read_fp8(kpages, vpages, kscales, vscales, block_table, seqlens, cu_seqlens,
+                             k, v, stream=None):
+    """C ``attn_sink_cache_read_fp8``: the last ``cu_seqlens[b+1] -
+    cu_seqlens[b]`` cached rows of every sequence into packed bf16 k, v
+    ``[T, Hkv, D]``."""
+    ts = (kpages, vpages, kscales, vscales, block_table, seqlens, cu_seqlens, k, v)
+    rc = _on_device("attn_sink_cache_read_fp8", ts, lambda: load().attn_sink_cache_read_fp8(
+        *[_ref(describe(t)) for t in ts], _stream(stream, k)))
+    _check(rc, "attn_sink_cache_read_fp8")
+
+
+def attn_sink_decode_paged_fp8(q, kpages, vpages, kscales, vscales, block_table, seqlens, sinks,
+                               window: int, scale: float, out, stream=None):
+    """C ``attn_sink_decode_paged_fp8``: single-token decode over the pools
+    that ``attn_sink_cache_append_fp8`` fills."""
+    ts = (q, kpages, vpages, kscales, vscales, block_table, seqlens, sinks, out)
+    rc = _on_device("attn_sink_decode_paged_fp8", ts, lambda: load().attn_sink_decode_paged_fp8(
+        *[_ref(describe(t)) for t in ts[:8]], int(window), float(scale), _ref(describe(out)),
+        _stream(stream, q)))
+    _check(rc, "attn_sink_decode_paged_fp8")
 
 
 def attn_sink_set_wait_limit_ns(ns: int):

@@ -14,8 +14,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libattnsink.so")
-SOURCES = ["api.cu", "fwd_tc.cu", "fwd_cudacore.cu", "decode.cu", "decode_noalloc.cu", "bwd.cu", "bwd_tc.cu"]
-HEADERS = ["ptx.cuh", "status.cuh", "kernels.h", "api_internal.h"]
+SOURCES = ["api.cu", "api_cache.cu", "fwd_tc.cu", "fwd_cudacore.cu", "decode.cu", "decode_noalloc.cu",
+           "decode_paged_fp8.cu", "cache_fp8.cu", "bwd.cu", "bwd_tc.cu"]
+HEADERS = ["ptx.cuh", "status.cuh", "e4m3.cuh", "kernels.h", "api_internal.h"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

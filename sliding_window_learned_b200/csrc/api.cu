@@ -85,7 +85,20 @@ int status_ptr(int **out) {
   return ATTN_OK;
 }
 
-namespace {
+int sm_count(int *out) {
+  static std::atomic<int> count[kMaxDevices];
+  int dev;
+  int rc = current_device(&dev);
+  if (rc) return rc;
+  int n = count[dev].load();
+  if (n == 0) {
+    const cudaError_t e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return fail_cuda(e, "cudaDeviceGetAttribute");
+    count[dev].store(n);
+  }
+  *out = n;
+  return ATTN_OK;
+}
 
 // A private stream-ordered pool per device that keeps freed blocks cached, so
 // repeated decode calls reuse their workspace without new mappings.
@@ -113,12 +126,13 @@ int workspace_pool(cudaMemPool_t *out) {
 }
 
 // ------------------------------------------------------------ validation
-const char *dtype_name(int32_t d) {
+static const char *dtype_name(int32_t d) {
   switch (d) {
     case ATTN_DTYPE_BF16: return "bf16";
     case ATTN_DTYPE_F32: return "f32";
     case ATTN_DTYPE_I32: return "i32";
     case ATTN_DTYPE_E4M3: return "e4m3";
+    case ATTN_DTYPE_E8M0: return "e8m0";
     default: return "unknown";
   }
 }
@@ -140,7 +154,8 @@ int check_tensor(const attn_tensor *t, const char *name, int32_t dtype, int ndim
     return fail(ATTN_EINVAL, "%s: innermost stride must be 1", name);
   for (int d = 0; d < ndim - 1; ++d) {
     if (t->stride[d] <= 0) return fail(ATTN_EINVAL, "%s: stride of dim %d must be positive", name, d);
-    const int64_t per16 = dtype == ATTN_DTYPE_E4M3 ? 16 : 8;   // elements per 16 bytes
+    // elements per 16 bytes
+    const int64_t per16 = (dtype == ATTN_DTYPE_E4M3 || dtype == ATTN_DTYPE_E8M0) ? 16 : 8;
     if (tma && t->stride[d] % per16 != 0)
       return fail(ATTN_EINVAL, "%s: stride of dim %d must be a multiple of %lld elements (16 bytes)", name,
                   d, (long long)per16);
@@ -149,6 +164,8 @@ int check_tensor(const attn_tensor *t, const char *name, int32_t dtype, int ndim
 }
 
 bool finite_pos(float x) { return isfinite(x) && x > 0.f; }
+
+namespace {
 
 int prep_fwd(const attn_tensor *q, const attn_tensor *k, const attn_tensor *v,
              const attn_tensor *sinks, int32_t window, float scale, attn_tensor *out,
@@ -413,6 +430,44 @@ cudaError_t make_tma_pages5d(void *map_out, const void *base, int64_t npages, in
   alignas(64) CUtensorMap map;
   const CUresult r = encode(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(base), dims,
                             strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
+  memcpy(map_out, &map, sizeof(CUtensorMap));
+  tma_cache_put(key, map);
+  return cudaSuccess;
+}
+
+cudaError_t make_tma_pages8(void *map_out, const void *base, int64_t npages, int64_t page, int64_t H,
+                            int64_t D, const int64_t strides_el[3], int box_rows) {
+  const tma_encode_fn encode = tma_encode();
+  if (!encode) return cudaErrorNotSupported;
+  if ((D != 64 && D % 128 != 0) || box_rows < 1 || box_rows > 256) return cudaErrorInvalidValue;
+  const int64_t C = D < 128 ? D : 128;
+  TmaKey key;
+  key.base = base;
+  key.d[0] = D;
+  key.d[1] = H;
+  key.d[2] = page;
+  key.d[3] = npages;
+  key.s[0] = strides_el[0];
+  key.s[1] = strides_el[1];
+  key.s[2] = strides_el[2];
+  key.box = box_rows;
+  key.elem = -1;                     // (the 5-D byte view; no other map has this)
+  if (tma_cache_get(key, map_out)) return cudaSuccess;
+  const cuuint64_t dims[5] = {static_cast<cuuint64_t>(C), static_cast<cuuint64_t>(page),
+                              static_cast<cuuint64_t>(D / C), static_cast<cuuint64_t>(H),
+                              static_cast<cuuint64_t>(npages)};
+  // byte strides of dims 1..4: position in page, chunk, head, page
+  const cuuint64_t strides[4] = {static_cast<cuuint64_t>(strides_el[1]), static_cast<cuuint64_t>(C),
+                                 static_cast<cuuint64_t>(strides_el[2]), static_cast<cuuint64_t>(strides_el[0])};
+  const cuuint32_t box[5] = {static_cast<cuuint32_t>(C), static_cast<cuuint32_t>(box_rows),
+                             static_cast<cuuint32_t>(D / C), 1, 1};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  alignas(64) CUtensorMap map;
+  const CUresult r = encode(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void *>(base), dims, strides,
+                            box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            C == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
   memcpy(map_out, &map, sizeof(CUtensorMap));

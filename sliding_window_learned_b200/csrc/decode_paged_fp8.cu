@@ -1,0 +1,808 @@
+// decode_paged_fp8.cu -- single-token decode over the 8-bit paged cache
+// (e4m3 codes, one power-of-two scale per position and kv head), with the
+// causal window and the learned sink.
+//
+// With x_j = scale*log2e * 2^ek_j * <q, ck_j> (codes ck, scale exponents ek, ev):
+//   O = sum_j 2^x_j 2^ev_j cv_j / ( sum_j 2^x_j + 2^(sink*log2e) )
+// The value scales differ from key to key over up to 236 binades, so folding
+// them into P would overflow or flush its f16.  The numerator therefore keeps
+// a reference of its own, over y_j = x_j + ev_j, beside the softmax's over x_j:
+//   N = sum_j 2^(y_j - m) cv_j,  L = sum_j 2^(x_j - M),  O = N 2^(m - M) / L.
+// Both references move lazily (only when an exponent would exceed 2^8), which a
+// warp vote decides: the common tile needs no shuffle.
+//
+// Two launches, no host synchronisation:
+//   split    persistent, one CTA per SM.  Every CTA reads the lengths and finds
+//            its own share: the key tiles of all sequences, one after another,
+//            are cut into E equal spans ("teams"), and one item is (span, kv
+//            head), heads fastest, so that the CTAs that run together read the
+//            heads of the same positions (whole DRAM bursts).  A span may
+//            end one sequence and begin others; a sequence that lies in one span
+//            is finished there (sink included), one that is cut leaves a partial
+//            (O_s, LSE_s) per span.
+//   combine  merges the spans of each cut sequence, in order, and adds the sink
+//            once; writes zeros for empty sequences.  Launched with programmatic
+//            dependence: its blocks are resident before the split ends.
+// At most two partials exist per span, whatever the lengths.
+//
+// Inside the split: a producer warp streams tiles of 16 keys per consumer warp
+// into a ring of stages; each lane looks after 16 keys' page, the boxes go by
+// TMA (min(page, 64) positions x all D channels of a head) and the 16 scale bytes by
+// a 16-byte asynchronous copy, all counted on the stage's barrier.  A consumer
+// warp owns 16 keys of the tile: e4m3 is converted to f16 in registers (exact)
+// and both products run on warp-level f16 MMAs (heads are the N = 8 dimension),
+// q in f16 under a power-of-two scale per head.  The work is bound by HBM: D + 1
+// bytes per key, kv head and K or V.
+#include <math.h>
+
+#include <type_traits>
+
+#include "e4m3.cuh"
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace attnsink {
+namespace {
+
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLog2e = 1.4426950408889634f;
+enum : int { kWhereFull = 401, kWhereEmpty = 402, kWhereMerge = 403 };
+
+// The numerator's P is f16, up to 2^15: kHeadroom keeps it as far from the
+// subnormals as the lazy reference (exponents up to kLazy above it) allows.
+constexpr float kLazy = 8.0f;
+constexpr float kHeadroom = 7.0f;
+constexpr float kNoMax = -1e30f;      // a reference nothing was seen against
+
+// ------------------------------------------------------------- workspace
+struct Workspace {
+  size_t off_info, off_lse, off_o, total;
+};
+
+__host__ __device__ inline size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+// Spans at most: as many as give every SM an item, or the smallest number of
+// rounds (up to four) that leaves at most a tenth of the SMs idle.
+int max_teams(int Hkv, int sms) {
+  int best = 1;
+  double used = 0;
+  for (int w = 1; w <= 4; ++w) {
+    const int t = static_cast<int>(static_cast<int64_t>(w) * sms / Hkv);
+    if (t < 1) continue;
+    const double u = static_cast<double>(t) * Hkv / (static_cast<double>(w) * sms);
+    if (u > used + 0.05) {
+      used = u;
+      best = t;
+    }
+    if (used >= 0.9) break;
+  }
+  return best;
+}
+
+Workspace layout(const PagedFp8Args &a, int teams) {
+  Workspace w;
+  size_t off = 0;
+  w.off_info = off;                                     // [teams] int2 (first sequence cut here, last span), [teams] = E
+  off = align256(off + sizeof(int2) * (teams + 1));
+  w.off_lse = off;                                      // [2 * teams][Hq]
+  off = align256(off + sizeof(float) * 2 * teams * a.Hq);
+  w.off_o = off;                                        // [2 * teams][Hq][D]
+  off = align256(off + sizeof(float) * 2 * teams * a.Hq * a.D);
+  w.total = off;
+  return w;
+}
+
+struct Params {
+  PagedFp8Args a;
+  int G, teams, page_shift, box_rows, box_shift;
+  float scale_log2;
+  int2 *info;
+  float *lse_part, *o_part;
+};
+
+// Keys [lo, n) of a sequence in tiles of TK starting at lo rounded down to a box.
+struct Range {
+  int n, vis0, start, tiles;
+};
+template <int TK>
+__device__ __forceinline__ Range range_of(const Params &p, int seqlen) {
+  Range r;
+  const long long cap = static_cast<long long>(p.a.max_pages) << p.page_shift;
+  r.n = static_cast<int>(min(static_cast<long long>(max(seqlen, 0)), cap));
+  r.vis0 = max(0, r.n - p.a.W);
+  r.start = r.vis0 & ~(p.box_rows - 1);
+  r.tiles = (r.n - r.start + TK - 1) / TK;
+  return r;
+}
+
+struct StageInfo {
+  int b, hk, dest, nvalid;             // dest: partial slot, or -1: the sequence is finished here
+  int nskip, flags, pad0, pad1;        // flags: 1 first tile of a piece, 2 last tile, 4 end of work
+};
+
+template <int D, int NT>
+struct Cfg {
+  // Consumer warps: twelve hide the conversion's latency; at D = 256 eight, as
+  // many as three 64 KB stages allow.
+  static constexpr int kCW = D == 256 ? 8 : 12;
+  // Two head tiles at D = 128: the q fragments live in shared memory (per
+  // warp), so that twelve warps keep within 128 registers each.
+  static constexpr bool kQInSmem = NT == 2 && D >= 128;
+  static constexpr int kTK = 16 * kCW;
+  static constexpr int kThreads = (kCW + 1) * 32;
+  static constexpr int kInner = D < 128 ? D : 128;          // bytes of a swizzled row
+  static constexpr int kChunks = D / kInner;
+  static constexpr int kTileBytes = kTK * D;
+  static constexpr int kStageBytes = 2 * kTileBytes;        // K then V
+  static constexpr int kScaleBytes = 2 * kTK;               // per stage: K then V
+  static constexpr int kQBytes = kQInSmem ? kCW * (D / 16) * NT * 32 * 8 : 0;
+  static constexpr int kFixed = 1024 /* alignment */ + kQBytes + 2 * kCW * NT * 8 * 8 + 512;
+  static constexpr int kStagesRaw = (232448 - kFixed) / (kStageBytes + kScaleBytes + 64);
+  static constexpr int kStages = kStagesRaw > 8 ? 8 : kStagesRaw;
+  static constexpr int kQOffset = kStages * kStageBytes;
+  static constexpr int kScaleOffset = kQOffset + kQBytes;
+  static constexpr int kInfoOffset = kScaleOffset + (kStages * kScaleBytes + 127) / 128 * 128;
+  // stage infos and barriers, the merge barrier, (m, M, L) per warp and head,
+  // scan scratch, abort flag
+  static constexpr int kTail = kStages * (32 + 16) + 8 + 3 * kCW * NT * 8 * 4 + 32 * 8 + 32;
+  static constexpr int kSmemBytes = kInfoOffset + kTail + 1024;
+  static_assert(kStages >= 3, "ring");
+  static_assert(kSmemBytes <= 232448, "shared-memory budget");
+  static_assert(kCW * 8 * D * 4 <= kStageBytes, "one merge pass fits a stage");
+  static_assert(kTK / 16 <= 16, "one lane per 16 keys of K and of V");
+};
+
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const WaitCtx &ctx, int where) {
+  const bool r = mbar_wait(bar, parity, ctx, where);
+  return __all_sync(0xffffffffu, r);
+}
+
+// 16 bytes global -> shared, or 16 zero bytes when !valid (nothing is read).
+__device__ __forceinline__ void copy16_async(void *dst, const void *src, bool valid) {
+  const int n = valid ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n) : "memory");
+}
+// The barrier gets one arrival when this thread's copies so far have landed.
+__device__ __forceinline__ void copy_async_arrive(uint64_t *bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void copy_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t f32x2_to_f16x2(uint32_t bf, float s) {
+  return pack_f16x2(__uint_as_float(bf << 16) * s, __uint_as_float(bf & 0xFFFF0000u) * s);
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
+    paged_fp8_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                           const __grid_constant__ Params p) {
+  using C = Cfg<D, NT>;
+  asm volatile("griddepcontrol.launch_dependents;");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem =
+      reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  StageInfo *info = reinterpret_cast<StageInfo *>(smem + C::kInfoOffset);
+  uint64_t *full = reinterpret_cast<uint64_t *>(info + C::kStages);
+  uint64_t *empty = full + C::kStages;
+  uint64_t *merge_bar = empty + C::kStages;
+  long long *scan = reinterpret_cast<long long *>(merge_bar + 1);   // [32]
+  float *merge_n = reinterpret_cast<float *>(scan + 32);            // numerator reference [kCW][NT*8]
+  float *merge_m = merge_n + C::kCW * NT * 8;                       // softmax reference
+  float *merge_l = merge_m + C::kCW * NT * 8;                       // softmax sum
+  int *abort_flag = reinterpret_cast<int *>(merge_l + C::kCW * NT * 8);
+  const PagedFp8Args &a = p.a;
+  const WaitCtx ctx{abort_flag, a.status, wait_limit_ns(a.status)};
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  // ------------------------------------------------------------------ plan
+  // Thread t counts the tiles of a run of sequences; a block-wide scan gives
+  // every run's first tile and the total.
+  const int per = (a.B + C::kThreads - 1) / C::kThreads;
+  const int run0 = min(a.B, static_cast<int>(threadIdx.x) * per), run1 = min(a.B, run0 + per);
+  long long mine = 0;
+  for (int b = run0; b < run1; ++b) mine += range_of<C::kTK>(p, a.seqlens[b]).tiles;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&full[s], 33);         // the producer's expect_tx, and its 32 lanes' scale copies
+      mbar_init(&empty[s], C::kCW);
+    }
+    mbar_init(merge_bar, C::kCW * 32);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) scan[warp] = incl;
+  __syncthreads();
+  long long before = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w <= C::kCW; ++w) {
+    const long long s = scan[w];
+    if (w < warp) before += s;
+    total += s;
+  }
+  const int E = static_cast<int>(min(static_cast<long long>(p.teams), total));   // spans in use
+  const int items = E * a.Hkv;
+  if (blockIdx.x == 0 && threadIdx.x == 0) p.info[p.teams] = make_int2(E, 0);
+  if (static_cast<int>(blockIdx.x) >= items) return;
+  auto span_start = [&](int j) { return static_cast<long long>(j) * total / E; };
+  // the run that holds the first tile of this CTA's first span
+  const long long first_tile = span_start(blockIdx.x / a.Hkv);
+  __syncthreads();                     // (every thread has read scan[])
+  if (mine > 0 && before <= first_tile && first_tile < before + mine) {
+    scan[0] = before;
+    scan[1] = run0;
+  }
+  __syncthreads();
+
+  if (warp == C::kCW) {
+    // -------------------------------------------------------------- producer
+    // One control flow for the whole warp: lane (kv, c) looks after keys
+    // 16c .. 16c+15 of K (kv = 0) or V (kv = 1).
+    if (lane == 0) {
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+    }
+    const int kv = lane >> 4, c = lane & 15;
+    const int rows = p.box_rows;
+    const bool active = c < C::kTK / 16;
+    const bool issues = active && (c * 16) % rows == 0;   // this lane's 16 keys start a box
+    const uint8_t *scales = kv ? a.vscales : a.kscales;
+    const int64_t sc_page = kv ? a.vs_s[0] : a.ks_s[0], sc_head = kv ? a.vs_s[1] : a.ks_s[1];
+    int slot = 0;
+    bool ok = true;
+    auto acquire = [&]() -> int {
+      const int s = slot % C::kStages;
+      const uint32_t use = static_cast<uint32_t>(slot / C::kStages);
+      bool good = true;
+      if (lane == 0 && slot >= C::kStages && !mbar_wait(&empty[s], (use & 1u) ^ 1u, ctx, kWhereEmpty)) good = false;
+      ok = ok && __shfl_sync(0xffffffffu, good, 0);
+      if (ok) ++slot;
+      return s;
+    };
+    // (b, base): a sequence and its first tile; items come in the spans' order,
+    // and the walk of one begins where its span does
+    int b_from = static_cast<int>(scan[1]);
+    long long base_from = scan[0];
+    for (int item = blockIdx.x; ok && item < items; item += gridDim.x) {
+      const int team = item / a.Hkv, hk = item - team * a.Hkv;
+      const long long t0 = span_start(team), t1 = span_start(team + 1);
+      int2 note = make_int2(-1, 0);    // the sequence that begins in this span and is cut by its end
+      int b = b_from;
+      long long base = base_from;
+      Range r = range_of<C::kTK>(p, a.seqlens[b]);
+      long long t = t0;
+      while (ok && t < t1) {
+        while (t >= base + r.tiles) {
+          base += r.tiles;
+          r = range_of<C::kTK>(p, a.seqlens[++b]);
+        }
+        if (t == t0) {
+          b_from = b;
+          base_from = base;
+        }
+        const int i0 = static_cast<int>(t - base);                               // first tile of the piece
+        const int i1 = static_cast<int>(min(static_cast<long long>(r.tiles), t1 - base));
+        const bool whole = i0 == 0 && i1 == r.tiles;
+        const int dest = whole ? -1 : 2 * team + (i0 == 0 ? 1 : 0);
+        if (i0 == 0 && i1 < r.tiles)
+          note = make_int2(b, static_cast<int>(((base + r.tiles) * E - 1) / total));   // the span of its last tile
+        const int *table = a.block_table + static_cast<int64_t>(b) * a.bt_s0;
+        auto page_of = [&](int i) -> int {   // pool page of this lane's 16 keys of tile i
+          const int key = r.start + i * C::kTK + c * 16;
+          if (!active || i >= i1 || key >= r.n) return -1;
+          const int pg = table[key >> p.page_shift];
+          return pg >= 0 && pg < a.npages ? pg : -1;
+        };
+        int pg_next = page_of(i0);
+        for (int i = i0; ok && i < i1; ++i) {
+          const int pg = pg_next;
+          pg_next = page_of(i + 1);          // (read a tile ahead: its latency overlaps the stage wait)
+          const int key0 = r.start + i * C::kTK;
+          const int nvalid = min(C::kTK, r.n - key0);
+          const int s = acquire();
+          if (!ok) break;
+          // only the boxes that hold a valid key are loaded; the rest of the
+          // stage keeps old bytes, which are masked
+          const int nbox = (nvalid + rows - 1) >> p.box_shift;
+          if (lane == 0) {
+            StageInfo &si = info[s];
+            si.b = b;
+            si.hk = hk;
+            si.dest = dest;
+            si.nvalid = nvalid;
+            si.nskip = max(0, r.vis0 - key0);
+            si.flags = (i == i0 ? 1 : 0) | (i == i1 - 1 ? 2 : 0);
+            mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(nbox) * rows * D * 2);
+          }
+          __syncwarp();
+          uint8_t *stage = smem + s * C::kStageBytes + kv * C::kTileBytes;
+          const int key = key0 + c * 16;
+          const int at = key & (a.page - 1);
+          // An entry outside the pool reads as a page of zero rows: the box is
+          // out of range and filled with zeros (it still delivers its bytes).
+          if (issues && c * 16 < nbox * rows)
+            tma_load_5d(stage + c * 16 * D, kv ? &tmV : &tmK, &full[s], 0, at, 0, hk, pg);
+          if (active && c * 16 < nvalid)
+            copy16_async(smem + C::kScaleOffset + s * C::kScaleBytes + kv * C::kTK + c * 16,
+                         scales + (pg < 0 ? 0 : pg * sc_page + hk * sc_head + at), pg >= 0);
+          copy_async_arrive(&full[s]);
+        }
+        t = base + i1;
+      }
+      if (hk == 0 && lane == 0) p.info[team] = note;
+    }
+    if (ok) {
+      const int s = acquire();
+      if (ok) {
+        if (lane == 0) {
+          info[s].flags = 4;
+          mbar_arrive(&full[s]);
+        }
+        __syncwarp();
+        copy_async_arrive(&full[s]);
+      }
+    }
+    // Every copy has landed before this warp leaves: the CTA's shared memory
+    // outlives them, also when the consumers gave up early (each wait is bounded
+    // by the fixed limit, whatever limit the other waits use).
+    copy_async_wait_all();
+    for (int x = max(0, slot - C::kStages); x < slot; ++x) {
+      const uint64_t w0 = globaltimer_ns();
+      while (!mbar_try_wait(&full[x % C::kStages], static_cast<uint32_t>(x / C::kStages) & 1u))
+        if (globaltimer_ns() - w0 > kWaitLimitNs) break;
+    }
+    __syncwarp();
+    return;
+  }
+
+  // ------------------------------------------------------------- consumers
+  const int g8 = lane >> 2;       // key row within an 8-row block of S^T
+  const int tig = lane & 3;       // heads 2*tig, 2*tig+1 of a head tile
+  const int key_w = warp * 16;    // this warp's keys within a tile
+  const int bs = p.box_shift;
+  // Byte offset of (key row, 16-byte unit u of the row): [box][chunk][row in
+  // box][kInner bytes], 128- or 64-byte swizzle.
+  const int krow = key_w + (lane & 7) + ((lane >> 3) & 1) * 8;
+  const uint32_t row_off =
+      D == 256 ? static_cast<uint32_t>((((krow >> bs) * C::kChunks) << (bs + 7)) + ((krow & (p.box_rows - 1)) << 7))
+               : static_cast<uint32_t>(krow * C::kInner);
+  const uint32_t chunk_stride = 128u << bs;                          // (D = 256)
+  const uint32_t swz = D == 64 ? (krow >> 1) & 3 : krow & 7;
+  auto unit_off = [&](int u) -> uint32_t {
+    if (D == 256) return row_off + (u >> 3) * chunk_stride + (((u & 7) ^ swz) << 4);
+    return row_off + ((u ^ swz) << 4);
+  };
+  uint32_t qf[C::kQInSmem ? 1 : D / 16][NT][2];   // B fragments of q^T per k-step and head tile
+  uint2 *qsm = reinterpret_cast<uint2 *>(smem + C::kQOffset) + warp * (D / 16) * NT * 32 + lane;
+  float o[D / 16][NT][4];                         // O^T accumulators: [d tile][head tile][fragment]
+  float sl[NT][2];                                // softmax scale of this lane's heads (with q's power of two)
+  float n_ref[NT][2];                             // numerator reference (one per head, same in every lane)
+  float m_ref[NT][2], l_run[NT][2];               // softmax reference and sum of this lane's keys
+  uint32_t merge_phase = 0;
+  auto consumers_meet = [&]() -> bool {
+    mbar_arrive(merge_bar);
+    const bool met = warp_wait(merge_bar, merge_phase & 1u, ctx, kWhereMerge);
+    ++merge_phase;
+    return met;
+  };
+  for (int slot = 0;; ++slot) {
+    const int s = slot % C::kStages;
+    if (!warp_wait(&full[s], static_cast<uint32_t>(slot / C::kStages) & 1u, ctx, kWhereFull)) break;
+    const StageInfo si = info[s];
+    if (si.flags & 4) break;
+    const uint32_t kbase = smem_u32(smem + s * C::kStageBytes);
+    const uint32_t vbase = kbase + C::kTileBytes;
+    if (si.flags & 1) {
+      // a piece begins: the grouped queries of this kv head, in f16 under a
+      // power of two per head that puts its largest magnitude in [2^13, 2^14)
+      // (exact for elements above max * 2^-27); k = 2t, 2t+1, 2t+8, 2t+9 of a
+      // k-step hold d = 4t .. 4t+3 of its 16, the order K's bytes arrive in
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        uint32_t x[D / 16][2];
+        const int hl = nt * 8 + g8;
+        const __nv_bfloat16 *qr = a.q + si.b * a.q_s[0] + (si.hk * p.G + hl) * a.q_s[1] + 4 * tig;
+        float mx = 0.f;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          x[kk][0] = x[kk][1] = 0u;
+          if (hl < p.G) {
+            x[kk][0] = *reinterpret_cast<const uint32_t *>(qr + kk * 16);
+            x[kk][1] = *reinterpret_cast<const uint32_t *>(qr + kk * 16 + 2);
+          }
+        }
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+          for (int f = 0; f < 2; ++f)
+            mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(x[kk][f] << 16)), fabsf(__uint_as_float(x[kk][f] & 0xFFFF0000u))));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        int e = 0;
+        // (at most 2^126, so that the scale itself stays finite: a smaller q
+        // only lies lower in f16's range)
+        if (mx > 0.f && mx < INFINITY) e = min(13 - ilogbf(mx), 126);
+        const float qs = ldexpf(1.f, e);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t q0 = f32x2_to_f16x2(x[kk][0], qs), q1 = f32x2_to_f16x2(x[kk][1], qs);
+          if constexpr (C::kQInSmem) {
+            qsm[(kk * NT + nt) * 32] = make_uint2(q0, q1);
+          } else {
+            qf[kk][nt][0] = q0;
+            qf[kk][nt][1] = q1;
+          }
+        }
+        // the lanes of head h (8 columns) are 4h .. 4h+3; this lane's S columns
+        // are heads 2*tig and 2*tig + 1
+        const float ms = ldexpf(p.scale_log2, -e);
+        sl[nt][0] = __shfl_sync(0xffffffffu, ms, 8 * tig);
+        sl[nt][1] = __shfl_sync(0xffffffffu, ms, 8 * tig + 4);
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          n_ref[nt][f] = m_ref[nt][f] = kNoMax;
+          l_run[nt][f] = 0.f;
+        }
+      }
+#pragma unroll
+      for (int dm = 0; dm < D / 16; ++dm)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int f = 0; f < 4; ++f) o[dm][nt][f] = 0.f;
+      if constexpr (C::kQInSmem) __syncwarp();
+    }
+    // a warp none of whose keys is visible has nothing to add
+    if (si.nvalid > key_w && si.nskip < key_w + 16) {
+      // ---- S^T[16 keys x 8*NT heads] = K_w q^T ----
+      float sacc[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int f = 0; f < 4; ++f) sacc[nt][f] = 0.f;
+#pragma unroll
+      for (int up = 0; up < D / 32; ++up) {
+        // matrices (keys 0-7 | 8-15) x (16-byte unit u | u+1): lane (g, t)
+        // receives d = 16u + 4t .. 4t+3 of keys g and g + 8
+        uint32_t w0, w1, w2, w3;
+        ldmatrix_x4(kbase + unit_off(2 * up + (lane >> 4)), w0, w1, w2, w3);
+        const uint2 k0 = e4m3x4_to_f16x2x2(w0), k1 = e4m3x4_to_f16x2x2(w1);
+        const uint2 k2 = e4m3x4_to_f16x2x2(w2), k3 = e4m3x4_to_f16x2x2(w3);
+        const int kk = 2 * up;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          uint2 qa, qb;
+          if constexpr (C::kQInSmem) {
+            qa = qsm[(kk * NT + nt) * 32];
+            qb = qsm[((kk + 1) * NT + nt) * 32];
+          } else {
+            qa = make_uint2(qf[kk][nt][0], qf[kk][nt][1]);
+            qb = make_uint2(qf[kk + 1][nt][0], qf[kk + 1][nt][1]);
+          }
+          mma_f16_16816(sacc[nt], k0.x, k1.x, k0.y, k1.y, qa.x, qa.y);
+          mma_f16_16816(sacc[nt], k2.x, k3.x, k2.y, k3.y, qb.x, qb.y);
+        }
+      }
+      // ---- softmax terms (no sink here) ----
+      const uint8_t *sck = smem + C::kScaleOffset + s * C::kScaleBytes + key_w + g8;
+      const float ks0 = scale_value(sck[0]), ks1 = scale_value(sck[8]);
+      const uint32_t vb0 = sck[C::kTK], vb1 = sck[C::kTK + 8];
+      const float ev0 = vb0 == 255u ? NAN : static_cast<float>(static_cast<int>(vb0) - 127);
+      const float ev1 = vb1 == 255u ? NAN : static_cast<float>(static_cast<int>(vb1) - 127);
+      const int i0 = key_w + g8, i1 = i0 + 8;
+      const bool in0 = i0 >= si.nskip && i0 < si.nvalid, in1 = i1 >= si.nskip && i1 < si.nvalid;
+      float x[NT][4], y[NT][4];
+      bool grow = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        x[nt][0] = in0 ? sacc[nt][0] * (sl[nt][0] * ks0) : -INFINITY;   // key g,     head 2*tig
+        x[nt][1] = in0 ? sacc[nt][1] * (sl[nt][1] * ks0) : -INFINITY;   // key g,     head 2*tig + 1
+        x[nt][2] = in1 ? sacc[nt][2] * (sl[nt][0] * ks1) : -INFINITY;   // key g + 8, head 2*tig
+        x[nt][3] = in1 ? sacc[nt][3] * (sl[nt][1] * ks1) : -INFINITY;   // key g + 8, head 2*tig + 1
+        y[nt][0] = in0 ? x[nt][0] + ev0 : -INFINITY;
+        y[nt][1] = in0 ? x[nt][1] + ev0 : -INFINITY;
+        y[nt][2] = in1 ? x[nt][2] + ev1 : -INFINITY;
+        y[nt][3] = in1 ? x[nt][3] + ev1 : -INFINITY;
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+          grow = grow || fmaxf(x[nt][f], x[nt][f + 2]) > m_ref[nt][f] + kLazy ||
+                 fmaxf(y[nt][f], y[nt][f + 2]) > n_ref[nt][f] + kLazy;
+      }
+      if (__any_sync(0xffffffffu, grow)) {
+        // a reference is left behind (always on a piece's first tile, rarely
+        // after it): move both up to the maxima seen
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+            const float m1 = fmaxf(m_ref[nt][f], fmaxf(x[nt][f], x[nt][f + 2]));
+            l_run[nt][f] *= ex2_approx(m_ref[nt][f] - m1);
+            m_ref[nt][f] = m1;
+            float n1 = fmaxf(y[nt][f], y[nt][f + 2]);
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, off));
+            n1 = fmaxf(n_ref[nt][f], n1);
+            const float al = ex2_approx(n_ref[nt][f] - n1);
+            n_ref[nt][f] = n1;
+#pragma unroll
+            for (int dm = 0; dm < D / 16; ++dm) {
+              o[dm][nt][f] *= al;
+              o[dm][nt][f + 2] *= al;
+            }
+          }
+      }
+      uint32_t pb[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        l_run[nt][0] += ex2_approx(x[nt][0] - m_ref[nt][0]) + ex2_approx(x[nt][2] - m_ref[nt][0]);
+        l_run[nt][1] += ex2_approx(x[nt][1] - m_ref[nt][1]) + ex2_approx(x[nt][3] - m_ref[nt][1]);
+        const float r0 = n_ref[nt][0] - kHeadroom, r1 = n_ref[nt][1] - kHeadroom;
+        // P^T fragments, transposed into the B operand of O^T += V^T P^T
+        pb[nt][0] = movmatrix_trans(pack_f16x2(ex2_approx(y[nt][0] - r0), ex2_approx(y[nt][1] - r1)));
+        pb[nt][1] = movmatrix_trans(pack_f16x2(ex2_approx(y[nt][2] - r0), ex2_approx(y[nt][3] - r1)));
+      }
+      // ---- O^T[D x 8*NT] += V_w^T P^T ----
+      // ldmatrix.trans of bytes taken as 16-bit pairs: lane (g, t) receives
+      // keys 2t, 2t+1 (2t+8, 2t+9) at d = 16u + 2g and 2g + 1; one byte permute
+      // makes key pairs per d, so O^T rows g and g + 8 of d tile u are d = 16u +
+      // 2g and 16u + 2g + 1.  Codes of keys outside [nskip, nvalid) may be
+      // anything (NaN included): on the tiles that have any they are zeroed here.
+      auto pv = [&](auto masked) {
+        uint32_t mlo = 0xFFFFFFFFu, mhi = 0xFFFFFFFFu;
+        if constexpr (decltype(masked)::value) {
+          const int ka = key_w + 2 * tig;
+          auto in = [&](int k) { return k >= si.nskip && k < si.nvalid; };
+          mlo = (in(ka) ? 0x0000FFFFu : 0u) | (in(ka + 1) ? 0xFFFF0000u : 0u);
+          mhi = (in(ka + 8) ? 0x0000FFFFu : 0u) | (in(ka + 9) ? 0xFFFF0000u : 0u);
+        }
+#pragma unroll
+        for (int up = 0; up < D / 32; ++up) {
+          uint32_t w0, w1, w2, w3;
+          ldmatrix_x4_trans(vbase + unit_off(2 * up + (lane >> 4)), w0, w1, w2, w3);
+          w0 = __byte_perm(w0, 0u, 0x3120);
+          w1 = __byte_perm(w1, 0u, 0x3120);
+          w2 = __byte_perm(w2, 0u, 0x3120);
+          w3 = __byte_perm(w3, 0u, 0x3120);
+          if constexpr (decltype(masked)::value) {
+            // (bytes: d even of keys k, k+1, then d odd of keys k, k+1)
+            const uint32_t blo = __byte_perm(mlo, 0u, 0x2020), bhi = __byte_perm(mhi, 0u, 0x2020);
+            w0 &= blo;
+            w1 &= bhi;
+            w2 &= blo;
+            w3 &= bhi;
+          }
+          const uint2 v0 = e4m3x4_to_f16x2x2(w0), v1 = e4m3x4_to_f16x2x2(w1);
+          const uint2 v2 = e4m3x4_to_f16x2x2(w2), v3 = e4m3x4_to_f16x2x2(w3);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_f16_16816(o[2 * up][nt], v0.x, v0.y, v1.x, v1.y, pb[nt][0], pb[nt][1]);
+            mma_f16_16816(o[2 * up + 1][nt], v2.x, v2.y, v3.x, v3.y, pb[nt][0], pb[nt][1]);
+          }
+        }
+      };
+      if (si.nskip <= key_w && si.nvalid >= key_w + 16)
+        pv(std::false_type{});
+      else
+        pv(std::true_type{});
+    }
+    // the stage is only read here: release it, but the last one of a piece only
+    // after the merge that reuses its memory
+    if (!(si.flags & 2)) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[s]);
+      continue;
+    }
+    // ---- a piece ends: merge the warps' states, write O or (O_s, LSE_s) ----
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        float M = m_ref[nt][f];
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+        float L = l_run[nt][f] * ex2_approx(m_ref[nt][f] - M);
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+        m_ref[nt][f] = M;
+        l_run[nt][f] = L;
+      }
+    if (!consumers_meet()) return;     // every warp is done with this stage
+    if (g8 == 0) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          const int at = warp * NT * 8 + nt * 8 + 2 * tig + f;
+          merge_n[at] = n_ref[nt][f] - kHeadroom;
+          merge_m[at] = m_ref[nt][f];
+          merge_l[at] = l_run[nt][f];
+        }
+    }
+    float *mbuf = reinterpret_cast<float *>(smem + s * C::kStageBytes);   // [warp][8 heads][D]
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      if (nt > 0 && !consumers_meet()) return;     // the previous pass is fully read
+      float *mw = mbuf + warp * 8 * D;
+#pragma unroll
+      for (int dm = 0; dm < D / 16; ++dm) {
+        const int d = dm * 16 + 2 * g8;
+        *reinterpret_cast<float2 *>(mw + 2 * tig * D + d) = make_float2(o[dm][nt][0], o[dm][nt][2]);
+        *reinterpret_cast<float2 *>(mw + (2 * tig + 1) * D + d) = make_float2(o[dm][nt][1], o[dm][nt][3]);
+      }
+      if (!consumers_meet()) return;
+      const int heads = min(p.G - nt * 8, 8);
+      for (int e = threadIdx.x; e < heads * (D / 4); e += C::kCW * 32) {
+        const int hl = e / (D / 4), d = (e - hl * (D / 4)) * 4, hh = nt * 8 + hl;
+        const int hq = si.hk * p.G + hh;
+        float M = kNoMax;
+#pragma unroll
+        for (int w = 0; w < C::kCW; ++w) M = fmaxf(M, merge_m[w * NT * 8 + hh]);
+        // the sink joins here if no other span holds keys of this sequence
+        float sink2 = -INFINITY;
+        if (si.dest < 0) {
+          sink2 = a.sinks[hq] * kLog2e;
+          M = fmaxf(M, sink2);
+        }
+        float den = si.dest < 0 ? ex2_approx(sink2 - M) : 0.f;
+        float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < C::kCW; ++w) {
+          const int at = w * NT * 8 + hh;
+          den += merge_l[at] * ex2_approx(merge_m[at] - M);
+          const float f = ex2_approx(merge_n[at] - M);
+          const float4 v = *reinterpret_cast<const float4 *>(mbuf + (w * 8 + hl) * D + d);
+          num.x = fmaf(f, v.x, num.x);
+          num.y = fmaf(f, v.y, num.y);
+          num.z = fmaf(f, v.z, num.z);
+          num.w = fmaf(f, v.w, num.w);
+        }
+        const float inv = den != 0.f ? 1.f / den : 0.f;
+        num = make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
+        if (si.dest < 0) {
+          __nv_bfloat16 *po = a.out + si.b * a.o_s[0] + hq * a.o_s[1] + d;
+          po[0] = __float2bfloat16_rn(num.x);
+          po[1] = __float2bfloat16_rn(num.y);
+          po[2] = __float2bfloat16_rn(num.z);
+          po[3] = __float2bfloat16_rn(num.w);
+        } else {
+          const size_t row = static_cast<size_t>(si.dest) * a.Hq + hq;
+          *reinterpret_cast<float4 *>(p.o_part + row * D + d) = num;
+          if (d == 0) p.lse_part[row] = (M + log2f(den)) * kLn2;
+        }
+      }
+    }
+    // the merge's generic accesses are ordered before the next TMA write
+    if (!consumers_meet()) return;
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[s]);
+  }
+}
+
+// ---------------------------------------------------------------- combine
+// One warp per (span that begins a cut sequence, query head), then one warp per
+// 32 sequences to write the rows of the empty ones.
+template <int D>
+__global__ void __launch_bounds__(128) paged_fp8_combine_kernel(const __grid_constant__ Params p) {
+  constexpr int kPer = D / 32;                      // channels per lane
+  const PagedFp8Args &a = p.a;
+  const int lane = threadIdx.x & 31;
+  const long long w = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+  const long long merges = static_cast<long long>(p.teams) * a.Hq;
+  if (w >= merges) {
+    const long long b0 = (w - merges) * 32;
+    if (b0 >= a.B) return;
+    const int n = b0 + lane < a.B ? min(a.seqlens[b0 + lane], a.max_pages << p.page_shift) : 1;
+    uint32_t empty = __ballot_sync(0xffffffffu, n <= 0);
+    while (empty) {
+      const long long b = b0 + __ffs(empty) - 1;
+      empty &= empty - 1;
+      for (int e = lane; e < a.Hq * D; e += 32) a.out[b * a.o_s[0] + (e / D) * a.o_s[1] + e % D] = __float2bfloat16_rn(0.f);
+    }
+    return;
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int team = static_cast<int>(w / a.Hq), hq = static_cast<int>(w - static_cast<long long>(team) * a.Hq);
+  const int E = min(p.info[p.teams].x, p.teams);
+  if (team >= E) return;
+  // (checked whole: a split whose waits ran out may not have written its note)
+  const int2 note = p.info[team];
+  if (note.x < 0 || note.x >= a.B || note.y <= team || note.y >= E) return;
+  const int parts = note.y - team + 1;
+  // part 0 is the span's own last piece, part i the first piece of span team + i
+  auto slot_of = [&](int i) { return static_cast<size_t>(i == 0 ? 2 * team + 1 : 2 * (team + i)) * a.Hq + hq; };
+  const float sink = a.sinks[hq];
+  float M = sink;
+  for (int i0 = 0; i0 < parts; i0 += 32) {
+    float ls = i0 + lane < parts ? p.lse_part[slot_of(i0 + lane)] : -INFINITY;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) ls = fmaxf(ls, __shfl_xor_sync(0xffffffffu, ls, off));
+    M = fmaxf(M, ls);
+  }
+  const float Mu = M == -INFINITY ? 0.f : M;
+  float den = __expf(sink - Mu);
+  float acc[kPer];
+#pragma unroll
+  for (int t = 0; t < kPer; ++t) acc[t] = 0.f;
+  for (int i0 = 0; i0 < parts; i0 += 32) {
+    const float wt = i0 + lane < parts ? __expf(p.lse_part[slot_of(i0 + lane)] - Mu) : 0.f;
+    float sum = wt;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    den += sum;
+    const int cnt = min(32, parts - i0);
+#pragma unroll 4
+    for (int i = 0; i < cnt; ++i) {              // spans in order
+      const float ws = __shfl_sync(0xffffffffu, wt, i);
+      const float *op = p.o_part + slot_of(i0 + i) * D + lane;
+#pragma unroll
+      for (int t = 0; t < kPer; ++t) acc[t] = fmaf(ws, op[32 * t], acc[t]);
+    }
+  }
+  const float inv = den != 0.f ? 1.f / den : 0.f;
+  __nv_bfloat16 *po = a.out + static_cast<int64_t>(note.x) * a.o_s[0] + hq * a.o_s[1] + lane;
+#pragma unroll
+  for (int t = 0; t < kPer; ++t) po[32 * t] = __float2bfloat16_rn(acc[t] * inv);
+}
+
+template <int D, int NT>
+cudaError_t launch(const Params &p, int sms, cudaStream_t stream) {
+  using C = Cfg<D, NT>;
+  const PagedFp8Args &a = p.a;
+  alignas(64) CUtensorMap mk, mv;
+  cudaError_t e;
+  if ((e = make_tma_pages8(&mk, a.kpages, a.npages, a.page, a.Hkv, D, a.kp_s, p.box_rows)) != cudaSuccess) return e;
+  if ((e = make_tma_pages8(&mv, a.vpages, a.npages, a.page, a.Hkv, D, a.vp_s, p.box_rows)) != cudaSuccess) return e;
+  auto split = paged_fp8_split_kernel<D, NT>;
+  if ((e = cudaFuncSetAttribute(split, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes)) != cudaSuccess)
+    return e;
+  const int64_t items = static_cast<int64_t>(p.teams) * a.Hkv;
+  split<<<static_cast<unsigned>(items < sms ? items : sms), C::kThreads, C::kSmemBytes, stream>>>(mk, mv, p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const int64_t warps = static_cast<int64_t>(p.teams) * a.Hq + (a.B + 31) / 32;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((warps + 3) / 4));
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_fp8_combine_kernel<D>, p);
+}
+
+}  // namespace
+
+size_t paged_fp8_workspace_bytes(const PagedFp8Args &a, int sms) { return layout(a, max_teams(a.Hkv, sms)).total; }
+
+cudaError_t launch_decode_paged_fp8(const PagedFp8Args &a, void *workspace, int sms, cudaStream_t stream) {
+  Params p;
+  p.a = a;
+  p.G = a.Hq / a.Hkv;
+  p.teams = max_teams(a.Hkv, sms);
+  p.page_shift = 0;
+  while ((1 << p.page_shift) < a.page) ++p.page_shift;
+  p.box_rows = a.page < 64 ? a.page : 64;
+  p.box_shift = p.page_shift < 6 ? p.page_shift : 6;
+  p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
+  const Workspace w = layout(a, p.teams);
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  p.info = reinterpret_cast<int2 *>(ws + w.off_info);
+  p.lse_part = reinterpret_cast<float *>(ws + w.off_lse);
+  p.o_part = reinterpret_cast<float *>(ws + w.off_o);
+  switch (a.D) {
+    case 64: return p.G <= 8 ? launch<64, 1>(p, sms, stream) : launch<64, 2>(p, sms, stream);
+    case 128: return p.G <= 8 ? launch<128, 1>(p, sms, stream) : launch<128, 2>(p, sms, stream);
+    case 256: return p.G <= 8 ? launch<256, 1>(p, sms, stream) : cudaErrorInvalidValue;
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace attnsink

@@ -2,6 +2,7 @@
 // launchers.  Arguments arrive here already validated; strides are in
 // elements and the innermost dimension of every tensor is contiguous.
 #pragma once
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -77,6 +78,38 @@ cudaError_t launch_bwd(const BwdArgs &a, void *workspace, cudaStream_t stream);
 cudaError_t launch_bwd_main_tc(const BwdArgs &a, const float *dsum, float *dq_acc, float *dk_acc, float *dv_acc,
                                cudaStream_t stream);
 
+// The 8-bit paged cache: e4m3 page pools [npages, page, Hkv, D], scale bytes
+// (e8m0) [npages, Hkv, page], block table [B, max_pages].  Packed row r of
+// sequence b (cu_seqlens[b] <= r < cu_seqlens[b+1]) is position
+// seqlens[b] - (cu_seqlens[b+1] - r).  append: k, v are read; read: k_out,
+// v_out are written (the same strides k_s, v_s: rows, heads).
+struct CacheArgs {
+  const __nv_bfloat16 *k = nullptr, *v = nullptr;
+  __nv_bfloat16 *k_out = nullptr, *v_out = nullptr;
+  int64_t k_s[2], v_s[2];
+  uint8_t *kpages, *vpages, *kscales, *vscales;
+  int64_t kp_s[3], vp_s[3], ks_s[2], vs_s[2];
+  const int *block_table, *seqlens, *cu_seqlens;
+  int64_t bt_s0, T;
+  int B, Hkv, D, page_shift, npages, max_pages;
+};
+cudaError_t launch_cache(const CacheArgs &a, bool append, cudaStream_t stream);
+
+// Decode over the 8-bit paged cache: q/out [B,Hq,D] bf16.
+struct PagedFp8Args {
+  const __nv_bfloat16 *q;
+  __nv_bfloat16 *out;
+  const uint8_t *kpages, *vpages, *kscales, *vscales;
+  int64_t q_s[2], o_s[2], kp_s[3], vp_s[3], ks_s[2], vs_s[2], bt_s0;
+  const int *block_table, *seqlens;
+  const float *sinks;
+  int B, Hq, Hkv, D, W, page, npages, max_pages;
+  float scale;
+  int *status;
+};
+size_t paged_fp8_workspace_bytes(const PagedFp8Args &a, int sms);
+cudaError_t launch_decode_paged_fp8(const PagedFp8Args &a, void *workspace, int sms, cudaStream_t stream);
+
 // Bytes of stream-ordered workspace one decode call needs (256-byte aligned
 // sections: plan, partial LSEs, partial outputs).
 size_t decode_workspace_bytes(const DecodeArgs &a);
@@ -110,5 +143,12 @@ cudaError_t make_tma_bshd(void *map_out, const void *base, int64_t d3, int64_t d
 // page <= 256.  Returns cudaErrorInvalidValue if the driver rejects it.
 cudaError_t make_tma_pages5d(void *map_out, const void *base, int64_t npages, int64_t page, int64_t H,
                              int64_t D, const int64_t strides_el[3]);
+// TMA descriptor of a byte page pool [npages, page, H, D] (element strides of
+// the first three dimensions; the last one contiguous) as 5-D (C channels,
+// position in page, C-channel chunk, head, page), C = min(D, 128), with a C-byte
+// swizzle (64 or 128) and boxes {C, box_rows, D/C, 1, 1}: in shared memory
+// [chunk][position][C bytes].  D is 64 or a multiple of 128.
+cudaError_t make_tma_pages8(void *map_out, const void *base, int64_t npages, int64_t page, int64_t H,
+                            int64_t D, const int64_t strides_el[3], int box_rows);
 
 }  // namespace attnsink
