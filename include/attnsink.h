@@ -140,6 +140,37 @@ int attn_sink_fwd_varlen(const attn_tensor *q, const attn_tensor *k, const attn_
                          attn_tensor *out, attn_tensor *lse, void *stream);
 
 /*
+ * attn_sink_fwd_varlen with keys before the queries: prompt chunks that continue
+ * sequences part of which was attended to earlier (page "Dao-AILab/
+ * flash-attention" contributor guide: the varlen path with cu_seqlens for
+ * queries and for keys).  For example the chunk's own keys behind the cached
+ * ones that attn_sink_cache_read_fp8 brought back.
+ *
+ *   q, out        [T, Hq, D]   bf16; the queries of sequence b are rows
+ *                 cu_seqlens_q[b] .. cu_seqlens_q[b+1]-1
+ *   k, v          [Tk, Hkv, D] bf16; its keys are rows cu_seqlens_k[b] ..
+ *                 cu_seqlens_k[b+1]-1, in order of position
+ *   cu_seqlens_q,
+ *   cu_seqlens_k  [B + 1] int32, DEVICE memory, as for attn_sink_fwd_varlen
+ *                 (clamped to [0, T] and [0, Tk]; empty sequences allowed).
+ *   max_seqlen_q  host int >= every sequence's number of queries.
+ *   sinks, window, scale: as for attn_sink_fwd.
+ *   lse           [Hq, T] f32 or NULL (innermost stride 1).
+ * With Lq queries and Lk keys, query i sits at position p = Lk - Lq + i and sees
+ * the keys max(0, p - W + 1) .. p.  Only the keys that some query sees need to be
+ * passed: the W - 1 before the chunk.  A query with p < 0 sees none: O = 0 and
+ * LSE = its sink.  Rows of q outside every sequence are left as they are in out
+ * and lse.  A NaN or infinity in a value row can reach queries of its own
+ * sequence that do not see it (never another sequence's).
+ * Supported head dims D: 64, 128, 256.  B = 0, T = 0 or max_seqlen_q = 0 is a
+ * no-op.  Runs on the tcgen05/TMEM tensor-core kernel of attn_sink_fwd.
+ */
+int attn_sink_fwd_extend(const attn_tensor *q, const attn_tensor *k, const attn_tensor *v,
+                         const attn_tensor *cu_seqlens_q, const attn_tensor *cu_seqlens_k,
+                         int32_t max_seqlen_q, const attn_tensor *sinks, int32_t window, float scale,
+                         attn_tensor *out, attn_tensor *lse, void *stream);
+
+/*
  * The same operation on a plain CUDA-core fp32 kernel (one warp per output
  * row).  Slow; it is an independent second implementation for verification
  * and debugging, with the same arguments and semantics as attn_sink_fwd, and

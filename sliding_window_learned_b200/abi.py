@@ -39,7 +39,7 @@ _DTYPES = {torch.bfloat16: ATTN_DTYPE_BF16, torch.float32: ATTN_DTYPE_F32,
 EXPORTS = ("attn_sink_fwd", "attn_sink_fwd_max_logit", "attn_sink_fwd_varlen", "attn_sink_bwd", "attn_sink_fwd_cudacore", "attn_sink_decode",
            "attn_sink_decode_chunked", "attn_sink_decode_paged", "attn_sink_decode_fp8",
            "attn_sink_decode_noalloc",
-           "attn_sink_cache_append_fp8", "attn_sink_cache_read_fp8", "attn_sink_decode_paged_fp8",
+           "attn_sink_fwd_extend", "attn_sink_cache_append_fp8", "attn_sink_cache_read_fp8", "attn_sink_decode_paged_fp8",
            "attn_sink_get_status", "attn_sink_set_wait_limit_ns", "attn_sink_fail_workspace_allocs",
            "attn_sink_strerror", "attn_sink_last_error")
 
@@ -93,6 +93,8 @@ def load() -> ctypes.CDLL:
             fn = getattr(lib, name)
             fn.argtypes = [P] * 9 + [V]
             fn.restype = ctypes.c_int
+        lib.attn_sink_fwd_extend.argtypes = [P, P, P, P, P, i32, P, i32, f32, P, P, V]
+        lib.attn_sink_fwd_extend.restype = ctypes.c_int
         lib.attn_sink_decode_paged_fp8.argtypes = [P] * 8 + [i32, f32, P, V]
         lib.attn_sink_decode_paged_fp8.restype = ctypes.c_int
         lib.attn_sink_get_status.argtypes = [V]
@@ -318,6 +320,18 @@ def attn_sink_decode_paged_fp8(q, kpages, vpages, kscales, vscales, block_table,
         *[_ref(describe(t)) for t in ts[:8]], int(window), float(scale), _ref(describe(out)),
         _stream(stream, q)))
     _check(rc, "attn_sink_decode_paged_fp8")
+
+
+def attn_sink_fwd_extend(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int, sinks, window: int,
+                         scale: float, out, lse=None, stream=None):
+    """C ``attn_sink_fwd_extend``: packed prompt chunks whose sequences have
+    earlier keys: q, out ``[T, Hq, D]`` by ``cu_seqlens_q``, k, v
+    ``[Tk, Hkv, D]`` by ``cu_seqlens_k``, lse ``[Hq, T]``."""
+    ts = (q, k, v, cu_seqlens_q, cu_seqlens_k, sinks, out, lse)
+    d = [_ref(describe(t)) for t in ts]
+    rc = _on_device("attn_sink_fwd_extend", ts, lambda: load().attn_sink_fwd_extend(
+        *d[:5], int(max_seqlen_q), d[5], int(window), float(scale), d[6], d[7], _stream(stream, q)))
+    _check(rc, "attn_sink_fwd_extend")
 
 
 def attn_sink_set_wait_limit_ns(ns: int):

@@ -1,6 +1,7 @@
 // api_cache.cu -- the C ABI of the 8-bit paged cache (declared in
 // include/attnsink.h): attn_sink_cache_append_fp8, attn_sink_cache_read_fp8,
-// attn_sink_decode_paged_fp8.  Argument checks and launches only.
+// attn_sink_decode_paged_fp8, and of attn_sink_fwd_extend, which continues a
+// prompt from rows read back.  Argument checks and launches only.
 #include <cuda_runtime.h>
 
 #include "../../include/attnsink.h"
@@ -20,15 +21,19 @@ int check_pools(const attn_tensor *kpages, const attn_tensor *vpages, const attn
                 const attn_tensor *vscales, const attn_tensor *block_table, const attn_tensor *seqlens, Pools *o) {
   int rc;
   if ((rc = check_tensor(kpages, "kpages", ATTN_DTYPE_E4M3, 4, true))) return rc;
+  o->P = kpages->shape[1];
+  o->D = kpages->shape[3];
+  if (o->P < 16 || o->P > 65536 || (o->P & (o->P - 1)))
+    return fail(ATTN_EUNSUPPORTED, "page size %lld must be a power of two in [16, 65536]", (long long)o->P);
+  if (o->D != 64 && o->D != 128 && o->D != 256)
+    return fail(ATTN_EUNSUPPORTED, "head dim %lld not supported (64, 128, 256)", (long long)o->D);
   if ((rc = check_tensor(vpages, "vpages", ATTN_DTYPE_E4M3, 4, true))) return rc;
   if ((rc = check_tensor(kscales, "kscales", ATTN_DTYPE_E8M0, 3, true))) return rc;
   if ((rc = check_tensor(vscales, "vscales", ATTN_DTYPE_E8M0, 3, true))) return rc;
   if ((rc = check_tensor(block_table, "block_table", ATTN_DTYPE_I32, 2, false))) return rc;
   if ((rc = check_tensor(seqlens, "seqlens", ATTN_DTYPE_I32, 1, false))) return rc;
   o->NB = kpages->shape[0];
-  o->P = kpages->shape[1];
   o->Hkv = kpages->shape[2];
-  o->D = kpages->shape[3];
   o->MP = block_table->shape[1];
   for (int d = 0; d < 4; ++d)
     if (vpages->shape[d] != kpages->shape[d]) return fail(ATTN_EINVAL, "vpages shape does not match kpages");
@@ -40,10 +45,6 @@ int check_pools(const attn_tensor *kpages, const attn_tensor *vpages, const attn
   if (o->NB < 1 || o->Hkv < 1) return fail(ATTN_EINVAL, "the pools need at least one page and one kv head");
   if (block_table->shape[0] != seqlens->shape[0]) return fail(ATTN_EINVAL, "block_table and seqlens must have B rows");
   if (seqlens->shape[0] > 1 && seqlens->stride[0] != 1) return fail(ATTN_EINVAL, "seqlens must be contiguous");
-  if (o->P < 16 || o->P > 65536 || (o->P & (o->P - 1)))
-    return fail(ATTN_EUNSUPPORTED, "page size %lld must be a power of two in [16, 65536]", (long long)o->P);
-  if (o->D != 64 && o->D != 128 && o->D != 256)
-    return fail(ATTN_EUNSUPPORTED, "head dim %lld not supported (64, 128, 256)", (long long)o->D);
   if (seqlens->shape[0] > (1 << 20) || o->NB > (1LL << 31) - 1 || o->MP > (1LL << 30) || o->MP * o->P > (1LL << 30) ||
       o->Hkv > 65535)
     return fail(ATTN_EUNSUPPORTED, "B, Hkv, the pool or pages per sequence * page size too large");
@@ -201,6 +202,82 @@ int attn_sink_decode_paged_fp8(const attn_tensor *q, const attn_tensor *kpages, 
   if (e != cudaSuccess) return fail_cuda(e, "attn_sink_decode_paged_fp8 launch");
   if (ef != cudaSuccess) return fail_cuda(ef, "decode workspace release");
   return ATTN_OK;
+}
+
+int attn_sink_fwd_extend(const attn_tensor *q, const attn_tensor *k, const attn_tensor *v,
+                         const attn_tensor *cu_seqlens_q, const attn_tensor *cu_seqlens_k, int32_t max_seqlen_q,
+                         const attn_tensor *sinks, int32_t window, float scale, attn_tensor *out, attn_tensor *lse,
+                         void *stream) {
+  clear_error();
+  int rc;
+  if ((rc = check_tensor(q, "q", ATTN_DTYPE_BF16, 3, true))) return rc;
+  if ((rc = check_tensor(k, "k", ATTN_DTYPE_BF16, 3, true))) return rc;
+  if ((rc = check_tensor(v, "v", ATTN_DTYPE_BF16, 3, true))) return rc;
+  if ((rc = check_tensor(cu_seqlens_q, "cu_seqlens_q", ATTN_DTYPE_I32, 1, false))) return rc;
+  if ((rc = check_tensor(cu_seqlens_k, "cu_seqlens_k", ATTN_DTYPE_I32, 1, false))) return rc;
+  if ((rc = check_tensor(sinks, "sinks", ATTN_DTYPE_F32, 1, false))) return rc;
+  if ((rc = check_tensor(out, "out", ATTN_DTYPE_BF16, 3, true))) return rc;
+  const int64_t T = q->shape[0], Hq = q->shape[1], D = q->shape[2], Tk = k->shape[0], Hkv = k->shape[1];
+  if (k->shape[2] != D) return fail(ATTN_EINVAL, "k head dim does not match q");
+  for (int d = 0; d < 3; ++d) {
+    if (v->shape[d] != k->shape[d]) return fail(ATTN_EINVAL, "v shape does not match k");
+    if (out->shape[d] != q->shape[d]) return fail(ATTN_EINVAL, "out shape does not match q");
+  }
+  const int64_t B = cu_seqlens_q->shape[0] - 1;
+  if (B < 0 || cu_seqlens_k->shape[0] != B + 1)
+    return fail(ATTN_EINVAL, "cu_seqlens_q and cu_seqlens_k need B + 1 >= 1 entries each");
+  if (B > 0 && (cu_seqlens_q->stride[0] != 1 || cu_seqlens_k->stride[0] != 1))
+    return fail(ATTN_EINVAL, "cu_seqlens_q and cu_seqlens_k must be contiguous");
+  if (sinks->shape[0] != Hq) return fail(ATTN_EINVAL, "sinks must have Hq = %lld entries", (long long)Hq);
+  if (Hq > 1 && sinks->stride[0] != 1) return fail(ATTN_EINVAL, "sinks must be contiguous");
+  if (Hq <= 0 || Hkv <= 0 || Hq % Hkv) return fail(ATTN_EINVAL, "Hq must be a positive multiple of Hkv");
+  if (window < 1) return fail(ATTN_EINVAL, "window must be >= 1");
+  if (max_seqlen_q < 0) return fail(ATTN_EINVAL, "max_seqlen_q must be >= 0");
+  if (!finite_pos(scale)) return fail(ATTN_EINVAL, "scale must be finite and > 0");
+  if (lse) {
+    if ((rc = check_tensor(lse, "lse", ATTN_DTYPE_F32, 2, false))) return rc;
+    if (lse->shape[0] != Hq || lse->shape[1] != T) return fail(ATTN_EINVAL, "lse must be [Hq, T]");
+  }
+  if (D != 64 && D != 128 && D != 256)
+    return fail(ATTN_EUNSUPPORTED, "head dim %lld not supported (64, 128, 256)", (long long)D);
+  if (B > 65535 || Hq > 65535 || T > (1LL << 30) || Tk > (1LL << 30))
+    return fail(ATTN_EUNSUPPORTED, "B and Hq must be <= 65535, T and Tk <= 2^30");
+  // no chunk is longer than T
+  const int64_t rows = max_seqlen_q < T ? max_seqlen_q : T;
+  if ((rows + 127) / 128 * B * Hq > 0x7FFFFFFF)
+    return fail(ATTN_EUNSUPPORTED, "ceil(max_seqlen_q / 128) * B * Hq must be < 2^31");
+  if (B == 0 || rows == 0) return ATTN_OK;
+  FwdArgs a;
+  a.q = q->data;
+  a.k = k->data;
+  a.v = v->data;
+  a.sinks = static_cast<const float *>(sinks->data);
+  a.out = out->data;
+  a.lse = lse ? static_cast<float *>(lse->data) : nullptr;
+  a.B = static_cast<int>(B);
+  a.L = static_cast<int>(rows);
+  a.T = static_cast<int>(T);
+  a.Tk = static_cast<int>(Tk);
+  a.Hq = static_cast<int>(Hq);
+  a.Hkv = static_cast<int>(Hkv);
+  a.D = static_cast<int>(D);
+  a.W = window < (1 << 30) ? window : (1 << 30);   // (positions are at least -2^30: no overflow)
+  a.scale = scale;
+  a.cu_seqlens = static_cast<const int *>(cu_seqlens_q->data);
+  a.cu_seqlens_k = static_cast<const int *>(cu_seqlens_k->data);
+  // one batch slice of rows each: its (unused) batch stride spans the slice
+  const attn_tensor *ts[4] = {q, k, v, out};
+  int64_t *ss[4] = {a.q_s, a.k_s, a.v_s, a.o_s};
+  for (int x = 0; x < 4; ++x) {
+    ss[x][0] = (ts[x]->shape[0] > 0 ? ts[x]->shape[0] : 1) * ts[x]->stride[0];
+    ss[x][1] = ts[x]->stride[0];
+    ss[x][2] = ts[x]->stride[1];
+  }
+  a.lse_s[0] = 0;
+  a.lse_s[1] = lse ? lse->stride[0] : 0;
+  if ((rc = status_ptr(&a.status))) return rc;
+  const cudaError_t e = launch_fwd_tc(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ATTN_OK : fail_cuda(e, "attn_sink_fwd_extend launch");
 }
 
 }  // extern "C"

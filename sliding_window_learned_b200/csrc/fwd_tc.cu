@@ -128,6 +128,10 @@ struct Params {
   int64_t o_sr, o_sh;
   float *max_logit;                        // [B, Hq] (stride ml_sb), kMaxLogit only
   int64_t ml_sb;
+  // kPrior only: the sequences' keys are rows cu_seqlens_k[b] ..
+  // cu_seqlens_k[b+1]-1 of [Tk, Hkv, D] tensors
+  const int *cu_seqlens_k;
+  int Tk;
 };
 
 // Warp-uniform bounded wait: every lane learns the same outcome, so the
@@ -338,9 +342,12 @@ __device__ __forceinline__ void atomic_max_float(float *addr, float v) {
     atomicMin(reinterpret_cast<unsigned int *>(addr), __float_as_uint(v));
 }
 
+// kPrior (with kPacked): a sequence has keys of its own row range, usually more
+// than queries: its queries are the last positions (row i sits at position
+// i + klen - len, and sees nothing where that is negative).
 // kMaxLogit: also the largest content logit scale*<q_i,k_j> over every row and
 // visible key of each (sequence, head), into Params::max_logit (atomic max).
-template <int D, int BN, int NH, bool kPacked, bool kMaxLogit>
+template <int D, int BN, int NH, bool kPacked, bool kMaxLogit, bool kPrior>
 __global__ void __launch_bounds__(Cfg<D, BN, NH>::kThreads, Cfg<D, BN, NH>::kCtasPerSm)
     fwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
@@ -384,6 +391,7 @@ __global__ void __launch_bounds__(Cfg<D, BN, NH>::kThreads, Cfg<D, BN, NH>::kCta
   // role skips it.
   struct Unit {
     int m0, h0, b, kt0, n_tiles, len, row0;
+    int pm0, klen, krow0;                  // position of row m0; the keys' count and first row
   };
   constexpr bool packed = kPacked;
   auto bc = [&](const Unit &t) { return packed ? 0 : t.b; };
@@ -404,9 +412,20 @@ __global__ void __launch_bounds__(Cfg<D, BN, NH>::kThreads, Cfg<D, BN, NH>::kCta
       t.row0 = 0;
       t.len = p.L;
     }
-    const int row_last = min(t.len - 1, t.m0 + kBM - 1);
-    t.kt0 = max(0, t.m0 - p.W + 1) / BN;
+    if constexpr (kPrior) {
+      t.krow0 = min(max(p.cu_seqlens_k[t.b], 0), p.Tk);
+      t.klen = min(max(p.cu_seqlens_k[t.b + 1], t.krow0), p.Tk) - t.krow0;
+      t.pm0 = t.m0 + t.klen - t.len;
+    } else {
+      t.krow0 = t.row0;
+      t.klen = t.len;
+      t.pm0 = t.m0;
+    }
+    const int row_last = min(t.klen - 1, t.pm0 + kBM - 1);   // (position of the tile's last row)
+    t.kt0 = max(0, t.pm0 - p.W + 1) / BN;
     t.n_tiles = t.m0 < t.len ? row_last / BN - t.kt0 + 1 : 0;
+    // a tile that sees no key still runs one, masked, for its zeros and LSE
+    if (kPrior && t.m0 < t.len && row_last < 0) t.n_tiles = 1;
     return t;
   };
 
@@ -502,7 +521,7 @@ __global__ void __launch_bounds__(Cfg<D, BN, NH>::kThreads, Cfg<D, BN, NH>::kCta
           mbar_arrive_expect_tx(&full[s], C::kTileBytes);
           uint8_t *dst = sRing + s * C::kTileBytes;
           for (int c = 0; c < C::kChunks; ++c)
-            tma_load_4d(dst + c * BN * 128, map, &full[s], c * 64, hk, t.row0 + kt * BN, bc(t));
+            tma_load_4d(dst + c * BN * 128, map, &full[s], c * 64, hk, t.krow0 + kt * BN, bc(t));
           ++slot;
         };
         for (int jj = 0; ok && jj < C::kSBuf && jj < t.n_tiles; ++jj) kv(&tmK, t.kt0 + jj);
@@ -653,7 +672,8 @@ __global__ void __launch_bounds__(Cfg<D, BN, NH>::kThreads, Cfg<D, BN, NH>::kCta
       ++ul;
       const int qb = ul & 1;
       const int h = t.h0 + w;
-      const int i = t.m0 + r;                        // query position
+      const int i = t.m0 + r;                        // query row of the sequence
+      const int pi = t.pm0 + r;                      // and its position
       float m_run = -INFINITY;                       // running max, log2 units
       float row_max = -INFINITY;                     // exact row maximum, log2 units
       float l_run = 0.f;                             // running denominator
@@ -669,9 +689,9 @@ __global__ void __launch_bounds__(Cfg<D, BN, NH>::kThreads, Cfg<D, BN, NH>::kCta
         const int kbase = (t.kt0 + j) * BN;
         // Tile-uniform test: does any (row, key) of this tile fall outside the
         // causal window or past the end of the sequence?
-        const bool edge = (kbase + BN - 1 > t.m0) || (kbase < t.m0 + kBM - p.W) || (kbase + BN > t.len);
-        const int lo = i - p.W + 1 - kbase;          // first visible column
-        const int hi = min(i, t.len - 1) - kbase;    // last visible column
+        const bool edge = (kbase + BN - 1 > t.pm0) || (kbase < t.pm0 + kBM - p.W) || (kbase + BN > t.klen);
+        const int lo = pi - p.W + 1 - kbase;         // first visible column
+        const int hi = min(pi, t.klen - 1) - kbase;  // last visible column
         // Per 32-column chunk, a warp-uniform class: every lane's visible
         // interval [lo, hi] covers the chunk (no mask), misses it (no work:
         // P = 0), or cuts it (per-element mask).
@@ -689,6 +709,28 @@ __global__ void __launch_bounds__(Cfg<D, BN, NH>::kThreads, Cfg<D, BN, NH>::kCta
                                  m_run, l_run, row_max, &pv_done[w], ctx)) {
           ok = false;
           break;
+        }
+        if constexpr (kPrior) {
+          // The value rows behind the sequence's last key are another
+          // sequence's: P is zero there, but 0 * NaN is not, so they are zeroed
+          // in the stage.  Only a unit's last tile has any, and its V is the
+          // last stage of the unit (2 n_tiles per unit).
+          if (kbase + BN > t.klen) {
+            const int vslot = 2 * (jg + t.n_tiles) - 1;
+            if (!warp_wait(&full[vslot % C::kStages], static_cast<uint32_t>(vslot / C::kStages) & 1u, ctx,
+                           kWhereFull)) {
+              ok = false;
+              break;
+            }
+            const int first = t.klen - kbase;        // (0 where the sequence has no key)
+            uint8_t *tile = sRing + (vslot % C::kStages) * C::kTileBytes;
+            const int units = (BN - first) * C::kChunks * 8;
+            for (int e = r; e < units; e += 128) {
+              const int row = first + e / (C::kChunks * 8), c = e % (C::kChunks * 8);
+              *reinterpret_cast<uint4 *>(tile + (c >> 3) * BN * 128 + row * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+          }
         }
         tmem_wait_st();
         tc_fence_before();
@@ -792,7 +834,7 @@ __global__ void __launch_bounds__(Cfg<D, BN, NH>::kThreads, Cfg<D, BN, NH>::kCta
   }
 }
 
-template <int D, int BN, int NH, bool kPacked, bool kMaxLogit = false>
+template <int D, int BN, int NH, bool kPacked, bool kMaxLogit = false, bool kPrior = false>
 cudaError_t launch(const FwdArgs &a, cudaStream_t stream) {
   using C = Cfg<D, BN, NH>;
   alignas(64) CUtensorMap mq, mk, mv, mo;
@@ -801,8 +843,13 @@ cudaError_t launch(const FwdArgs &a, cudaStream_t stream) {
   const int64_t nb = a.cu_seqlens != nullptr ? 1 : a.B;
   const int64_t nrow = a.cu_seqlens != nullptr ? a.T : a.L;
   if ((e = make_tma_bshd(&mq, a.q, nb, nrow, a.Hq, D, a.q_s, kBM)) != cudaSuccess) return e;
-  if ((e = make_tma_bshd(&mk, a.k, nb, nrow, a.Hkv, D, a.k_s, BN)) != cudaSuccess) return e;
-  if ((e = make_tma_bshd(&mv, a.v, nb, nrow, a.Hkv, D, a.v_s, BN)) != cudaSuccess) return e;
+  // (no key at all: K and V are maps over Q, every row of which is masked)
+  const bool no_keys = kPrior && a.Tk == 0;
+  const int64_t krow = kPrior && !no_keys ? a.Tk : nrow;
+  if ((e = make_tma_bshd(&mk, no_keys ? a.q : a.k, nb, krow, a.Hkv, D, no_keys ? a.q_s : a.k_s, BN)) != cudaSuccess)
+    return e;
+  if ((e = make_tma_bshd(&mv, no_keys ? a.q : a.v, nb, krow, a.Hkv, D, no_keys ? a.q_s : a.v_s, BN)) != cudaSuccess)
+    return e;
   if ((e = make_tma_bshd(&mo, a.out, nb, nrow, a.Hq, D, a.o_s, kBM)) != cudaSuccess) return e;
   Params p;
   p.L = a.L;
@@ -820,6 +867,8 @@ cudaError_t launch(const FwdArgs &a, cudaStream_t stream) {
   p.status = a.status;
   p.cu_seqlens = a.cu_seqlens;
   p.T = a.T;
+  p.cu_seqlens_k = a.cu_seqlens_k;
+  p.Tk = a.Tk;
   p.out = static_cast<__nv_bfloat16 *>(a.out);
   p.o_sr = a.o_s[1];
   p.o_sh = a.o_s[2];
@@ -829,7 +878,7 @@ cudaError_t launch(const FwdArgs &a, cudaStream_t stream) {
     // every entry starts at -inf; the kernel's units raise it
     if ((e = launch_max_logit_init(a.max_logit, a.ml_sb, a.B, a.Hq, stream)) != cudaSuccess) return e;
   }
-  auto kern = fwd_tc_kernel<D, BN, NH, kPacked, kMaxLogit>;
+  auto kern = fwd_tc_kernel<D, BN, NH, kPacked, kMaxLogit, kPrior>;
   static bool attr_set[64] = {};  // once per device (per instantiation)
   int dev = 0;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
@@ -865,6 +914,14 @@ cudaError_t launch_fwd_tc(const FwdArgs &a, cudaStream_t stream) {
   const bool packed = a.cu_seqlens != nullptr;
   const bool ml = a.max_logit != nullptr;   // (batched inputs only)
   if (packed && ml) return cudaErrorInvalidValue;
+  if (a.cu_seqlens_k != nullptr) {
+    switch (a.D) {
+      case 64: return launch<64, 64, 1, true, false, true>(a, stream);
+      case 128: return launch<128, 64, 1, true, false, true>(a, stream);
+      case 256: return launch<256, 64, 1, true, false, true>(a, stream);
+      default: return cudaErrorInvalidValue;
+    }
+  }
   switch (a.D) {
     case 64:
       if (packed) return launch<64, 64, 1, true>(a, stream);

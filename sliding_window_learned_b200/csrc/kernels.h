@@ -27,6 +27,11 @@ struct FwdArgs {
   // head stride).  Null: the [B, L] batch above.
   const int *cu_seqlens = nullptr;
   int T = 0;
+  // Packed sequences whose keys have rows of their own (k/v [Tk,Hkv,D], sequence
+  // b's are cu_seqlens_k[b] .. cu_seqlens_k[b+1]-1; its queries are the last
+  // positions).  Null: keys and queries share cu_seqlens.
+  const int *cu_seqlens_k = nullptr;
+  int Tk = 0;
   // Largest content logit per (batch, query head): [B, Hq] f32 (row stride
   // ml_sb), batched inputs only; null: not computed.
   float *max_logit = nullptr;

@@ -125,3 +125,32 @@ def test_no_page_is_refused_and_no_work_is_not(lib, op):
     assert _call(lib, op, a) == abi.ATTN_OK
     if op != "decode":
         assert _call(lib, op, _good(T=0)) == abi.ATTN_OK
+
+
+def _extend(lib, **over):
+    a = dict(q=_t([50, 8, 128]), k=_t([90, 2, 128]), v=_t([90, 2, 128]), cq=_t([4], I32), ck=_t([4], I32), mq=50,
+             s=_t([8], F32), W=100, scale=0.1, out=_t([50, 8, 128]), lse=_t([8, 50], F32))
+    a.update(over)
+    r = lambda n: ctypes.byref(a[n]) if a[n] is not None else None  # noqa: E731
+    return lib.attn_sink_fwd_extend(r("q"), r("k"), r("v"), r("cq"), r("ck"), a["mq"], r("s"), a["W"], a["scale"],
+                                    r("out"), r("lse"), None)
+
+
+@pytest.mark.parametrize("over", [
+    dict(q=_t([50, 8, 128], F32)), dict(k=_t([90, 2, 64])), dict(v=_t([91, 2, 128])), dict(cq=_t([5], I32)),
+    dict(ck=_t([4], F32)), dict(ck=_t([4], I32, strides=[2])), dict(cq=_t([0], I32), ck=_t([0], I32)), dict(mq=-1),
+    dict(s=_t([7], F32)), dict(W=0), dict(scale=0.0), dict(out=_t([49, 8, 128])), dict(lse=_t([50, 8], F32)),
+    dict(k=_t([90, 3, 128]), v=_t([90, 3, 128])), dict(k=_t([90, 2, 128], strides=[260, 128, 1])),
+    dict(q=None), dict(out=_t([50, 8, 128], ptr=0x10008))])
+def test_extend_arguments_are_checked(lib, over):
+    assert _extend(lib, **over) == abi.ATTN_EINVAL, abi.attn_sink_last_error()
+
+
+def test_extend_sizes(lib):
+    bad = dict(q=_t([50, 8, 96]), k=_t([90, 2, 96]), v=_t([90, 2, 96]), out=_t([50, 8, 96]))
+    assert _extend(lib, **bad) == abi.ATTN_EUNSUPPORTED
+    long = dict(q=_t([1 << 30, 8, 128]), out=_t([1 << 30, 8, 128]), lse=None, mq=1 << 30, cq=_t([60001], I32),
+                ck=_t([60001], I32))
+    assert _extend(lib, **long) == abi.ATTN_EUNSUPPORTED
+    assert _extend(lib, mq=0) == abi.ATTN_OK
+    assert _extend(lib, cq=_t([1], I32), ck=_t([1], I32)) == abi.ATTN_OK
