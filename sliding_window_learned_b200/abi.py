@@ -5,6 +5,9 @@ structs (device pointer, dtype, shape, strides) and passed to the library,
 which runs every step on the GPU.  There is no CPU fallback: if the library
 is missing or a call fails, an exception is raised.
 
+The calls of the 8-bit cache, whose kernels can be shorter than this marshalling,
+go through _binding.so (csrc/binding.cpp), which does the same in C++.
+
 The functions carry the C names.  ``stream`` defaults to torch's current CUDA
 stream on the tensors' device.
 """
@@ -273,18 +276,26 @@ def attn_sink_decode_noalloc(q, kcache, vcache, seqlens, sinks, window: int, sca
     _check(rc, "attn_sink_decode_noalloc")
 
 
-def _on_device(where: str, tensors, call):
-    """Run ``call`` with the tensors' device current, after checking that all
-    of them (None aside) are on one CUDA device: the library reads the pointers
-    on the device and cannot check where they lead."""
-    dev = tensors[0].get_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev or dev < 0:
-            raise ValueError(f"{where}: tensors must be on one CUDA device")
-    if dev == torch.cuda.current_device():
-        return call()
-    with torch.cuda.device(dev):
-        return call()
+_native = None
+
+
+def _binding():
+    """_binding.so: marshals the arguments of the serving calls in C++."""
+    global _native
+    if _native is None:
+        load()
+        try:
+            from . import _binding as native
+        except ImportError as e:
+            raise ImportError(f"_binding.so is not built ({e}); run "
+                              "`python -m sliding_window_learned_b200.build`") from e
+        _native = native
+    return _native
+
+
+def _raw(stream):
+    """None (the tensors' current stream) or a cudaStream_t as an int."""
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else stream
 
 
 def attn_sink_cache_append_fp8(k, v, block_table, seqlens, cu_seqlens, kpages, vpages, kscales,
@@ -294,10 +305,10 @@ def attn_sink_cache_append_fp8(k, v, block_table, seqlens, cu_seqlens, kpages, v
     ``[NB, P, Hkv, D]``) and their scales kscales, vscales
     (``torch.float8_e8m0fnu`` ``[NB, Hkv, P]``), as the last positions of each
     sequence (``seqlens`` counts them already)."""
-    ts = (k, v, block_table, seqlens, cu_seqlens, kpages, vpages, kscales, vscales)
-    rc = _on_device("attn_sink_cache_append_fp8", ts, lambda: load().attn_sink_cache_append_fp8(
-        *[_ref(describe(t)) for t in ts], _stream(stream, k)))
-    _check(rc, "attn_sink_cache_append_fp8")
+    rc = (_native or _binding()).cache_append(_raw(stream), k, v, block_table, seqlens, cu_seqlens, kpages,
+                                              vpages, kscales, vscales)
+    if rc:
+        _check(rc, "attn_sink_cache_append_fp8")
 
 
 def attn_sink_cache_read_fp8(kpages, vpages, kscales, vscales, block_table, seqlens, cu_seqlens,
@@ -305,21 +316,20 @@ def attn_sink_cache_read_fp8(kpages, vpages, kscales, vscales, block_table, seql
     """C ``attn_sink_cache_read_fp8``: the last ``cu_seqlens[b+1] -
     cu_seqlens[b]`` cached rows of every sequence into packed bf16 k, v
     ``[T, Hkv, D]``."""
-    ts = (kpages, vpages, kscales, vscales, block_table, seqlens, cu_seqlens, k, v)
-    rc = _on_device("attn_sink_cache_read_fp8", ts, lambda: load().attn_sink_cache_read_fp8(
-        *[_ref(describe(t)) for t in ts], _stream(stream, k)))
-    _check(rc, "attn_sink_cache_read_fp8")
+    rc = (_native or _binding()).cache_read(_raw(stream), kpages, vpages, kscales, vscales, block_table, seqlens,
+                                            cu_seqlens, k, v)
+    if rc:
+        _check(rc, "attn_sink_cache_read_fp8")
 
 
 def attn_sink_decode_paged_fp8(q, kpages, vpages, kscales, vscales, block_table, seqlens, sinks,
                                window: int, scale: float, out, stream=None):
     """C ``attn_sink_decode_paged_fp8``: single-token decode over the pools
     that ``attn_sink_cache_append_fp8`` fills."""
-    ts = (q, kpages, vpages, kscales, vscales, block_table, seqlens, sinks, out)
-    rc = _on_device("attn_sink_decode_paged_fp8", ts, lambda: load().attn_sink_decode_paged_fp8(
-        *[_ref(describe(t)) for t in ts[:8]], int(window), float(scale), _ref(describe(out)),
-        _stream(stream, q)))
-    _check(rc, "attn_sink_decode_paged_fp8")
+    rc = (_native or _binding()).decode_paged(_raw(stream), q, kpages, vpages, kscales, vscales, block_table,
+                                              seqlens, sinks, window, scale, out)
+    if rc:
+        _check(rc, "attn_sink_decode_paged_fp8")
 
 
 def attn_sink_fwd_extend(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int, sinks, window: int,
@@ -327,11 +337,10 @@ def attn_sink_fwd_extend(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int,
     """C ``attn_sink_fwd_extend``: packed prompt chunks whose sequences have
     earlier keys: q, out ``[T, Hq, D]`` by ``cu_seqlens_q``, k, v
     ``[Tk, Hkv, D]`` by ``cu_seqlens_k``, lse ``[Hq, T]``."""
-    ts = (q, k, v, cu_seqlens_q, cu_seqlens_k, sinks, out, lse)
-    d = [_ref(describe(t)) for t in ts]
-    rc = _on_device("attn_sink_fwd_extend", ts, lambda: load().attn_sink_fwd_extend(
-        *d[:5], int(max_seqlen_q), d[5], int(window), float(scale), d[6], d[7], _stream(stream, q)))
-    _check(rc, "attn_sink_fwd_extend")
+    rc = (_native or _binding()).fwd_extend(_raw(stream), q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, sinks,
+                                            window, scale, out, lse)
+    if rc:
+        _check(rc, "attn_sink_fwd_extend")
 
 
 def attn_sink_set_wait_limit_ns(ns: int):

@@ -1,4 +1,5 @@
-"""Builds libattnsink.so in-tree with nvcc for sm_100a.
+"""Builds libattnsink.so in-tree with nvcc for sm_100a, and the Python binding
+of its shortest calls (_binding.so, g++, against torch's headers).
 
 Usage:  python -m sliding_window_learned_b200.build [--verbose-ptxas]
 """
@@ -9,11 +10,13 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libattnsink.so")
+BINDING = os.path.join(HERE, "_binding.so")
 SOURCES = ["api.cu", "api_cache.cu", "fwd_tc.cu", "fwd_cudacore.cu", "decode.cu", "decode_noalloc.cu",
            "decode_paged_fp8.cu", "cache_fp8.cu", "bwd.cu", "bwd_tc.cu"]
 HEADERS = ["ptx.cuh", "status.cuh", "e4m3.cuh", "kernels.h", "api_internal.h"]
@@ -36,8 +39,35 @@ def _stale() -> bool:
     return any(os.path.getmtime(p) > t for p in deps if os.path.exists(p))
 
 
+def build_binding(force: bool = False) -> str:
+    """_binding.so: csrc/binding.cpp against torch's headers and libattnsink.so."""
+    src = os.path.join(CSRC, "binding.cpp")
+    header = os.path.join(os.path.dirname(HERE), "include", "attnsink.h")
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) > max(
+            os.path.getmtime(src), os.path.getmtime(header)):
+        return BINDING
+    import torch
+    top = os.path.dirname(torch.__file__)
+    nvcc = _nvcc()
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-isystem", os.path.join(top, "include"),
+           "-isystem", os.path.join(top, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include"),
+           "-isystem", sysconfig.get_paths()["include"], src, "-o", tmp,
+           "-L", HERE, "-l:libattnsink.so", "-Wl,-rpath,$ORIGIN",
+           "-L", os.path.join(top, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"binding build failed:\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, ptxas_verbose: bool = False) -> str:
     if not force and not _stale():
+        build_binding()
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
@@ -64,6 +94,7 @@ def build(force: bool = False, ptxas_verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    build_binding(force)
     return LIB
 
 
