@@ -105,7 +105,9 @@ int cache_call(const attn_tensor *k, const attn_tensor *v, const attn_tensor *kp
   a.page_shift = o.shift;
   a.npages = static_cast<int>(o.NB);
   a.max_pages = static_cast<int>(o.MP);
-  const cudaError_t e = launch_cache(a, append, static_cast<cudaStream_t>(stream));
+  int sms;
+  if ((rc = sm_count(&sms))) return rc;
+  const cudaError_t e = launch_cache(a, append, sms, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ATTN_OK : fail_cuda(e, name);
 }
 

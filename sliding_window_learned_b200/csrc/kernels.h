@@ -97,8 +97,11 @@ struct CacheArgs {
   const int *block_table, *seqlens, *cu_seqlens;
   int64_t bt_s0, T;
   int B, Hkv, D, page_shift, npages, max_pages;
+  // (set by the launch) vectors between two iterations of a warp, as rows and heads
+  int64_t stride = 0, stride_rows = 0;
+  int stride_heads = 0;
 };
-cudaError_t launch_cache(const CacheArgs &a, bool append, cudaStream_t stream);
+cudaError_t launch_cache(const CacheArgs &a, bool append, int sms, cudaStream_t stream);
 
 // Decode over the 8-bit paged cache: q/out [B,Hq,D] bf16.
 struct PagedFp8Args {
