@@ -25,7 +25,7 @@
 //            dependence: its blocks are resident before the split ends.
 // At most two partials exist per span, whatever the lengths.
 //
-// Inside the split: a producer warp streams tiles of 16 keys per consumer warp
+// Inside the split: producer warps stream tiles of 16 keys per consumer warp
 // into a ring of stages; each lane looks after 16 keys' page, the boxes go by
 // TMA (min(page, 64) positions x all D channels of a head) and the 16 scale bytes by
 // a 16-byte asynchronous copy, all counted on the stage's barrier.  A consumer
@@ -129,7 +129,12 @@ struct Cfg {
   // warp), so that twelve warps keep within 128 registers each.
   static constexpr bool kQInSmem = NT == 2 && D >= 128;
   static constexpr int kTK = 16 * kCW;
-  static constexpr int kThreads = (kCW + 1) * 32;
+  // Producer warps: each issues the copies of its share of the tile's keys (a
+  // warp issues its lanes' TMA copies one after another).
+  static constexpr int kPW = 4;
+  static constexpr int kShare = kTK / 16 / kPW;             // 16-key chunks of one producer warp
+  static constexpr int kWarps = kCW + kPW;
+  static constexpr int kThreads = kWarps * 32;
   static constexpr int kInner = D < 128 ? D : 128;          // bytes of a swizzled row
   static constexpr int kChunks = D / kInner;
   static constexpr int kTileBytes = kTK * D;
@@ -149,7 +154,7 @@ struct Cfg {
   static_assert(kStages >= 3, "ring");
   static_assert(kSmemBytes <= 232448, "shared-memory budget");
   static_assert(kCW * 8 * D * 4 <= kStageBytes, "one merge pass fits a stage");
-  static_assert(kTK / 16 <= 16, "one lane per 16 keys of K and of V");
+  static_assert(kShare * kPW * 16 == kTK && kShare <= 16, "one lane per 16 keys of K and of V");
 };
 
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const WaitCtx &ctx, int where) {
@@ -204,7 +209,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
   for (int b = run0; b < run1; ++b) mine += range_of<C::kTK>(p, a.seqlens[b]).tiles;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(&full[s], 33);         // the producer's expect_tx, and its 32 lanes' scale copies
+      mbar_init(&full[s], 1 + 32 * C::kPW);   // one expect_tx, and every producer lane's scale copies
       mbar_init(&empty[s], C::kCW);
     }
     mbar_init(merge_bar, C::kCW * 32);
@@ -221,7 +226,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
   __syncthreads();
   long long before = incl - mine, total = 0;
 #pragma unroll
-  for (int w = 0; w <= C::kCW; ++w) {
+  for (int w = 0; w < C::kWarps; ++w) {
     const long long s = scan[w];
     if (w < warp) before += s;
     total += s;
@@ -240,17 +245,20 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
   }
   __syncthreads();
 
-  if (warp == C::kCW) {
-    // -------------------------------------------------------------- producer
-    // One control flow for the whole warp: lane (kv, c) looks after keys
-    // 16c .. 16c+15 of K (kv = 0) or V (kv = 1).
-    if (lane == 0) {
+  if (warp >= C::kCW) {
+    // ------------------------------------------------------------- producers
+    // One control flow for every producer warp: lane (kv, c) looks after keys
+    // 16c .. 16c+15 of K (kv = 0) or V (kv = 1), c in the warp's share; the first
+    // warp's lane 0 also writes the stage's description.
+    const int pw = warp - C::kCW;
+    const bool lead = pw == 0 && lane == 0;
+    if (lead) {
       tma_prefetch_desc(&tmK);
       tma_prefetch_desc(&tmV);
     }
-    const int kv = lane >> 4, c = lane & 15;
+    const int kv = lane >> 4, c = pw * C::kShare + (lane & 15);
     const int rows = p.box_rows;
-    const bool active = c < C::kTK / 16;
+    const bool active = (lane & 15) < C::kShare;
     const bool issues = active && (c * 16) % rows == 0;   // this lane's 16 keys start a box
     const uint8_t *scales = kv ? a.vscales : a.kscales;
     const int64_t sc_page = kv ? a.vs_s[0] : a.ks_s[0], sc_head = kv ? a.vs_s[1] : a.ks_s[1];
@@ -310,7 +318,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           // only the boxes that hold a valid key are loaded; the rest of the
           // stage keeps old bytes, which are masked
           const int nbox = (nvalid + rows - 1) >> p.box_shift;
-          if (lane == 0) {
+          if (lead) {
             StageInfo &si = info[s];
             si.b = b;
             si.hk = hk;
@@ -335,12 +343,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         }
         t = base + i1;
       }
-      if (hk == 0 && lane == 0) p.info[team] = note;
+      if (hk == 0 && lead) p.info[team] = note;
     }
     if (ok) {
       const int s = acquire();
       if (ok) {
-        if (lane == 0) {
+        if (lead) {
           info[s].flags = 4;
           mbar_arrive(&full[s]);
         }
@@ -461,11 +469,16 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     // a warp none of whose keys is visible has nothing to add
     if (si.nvalid > key_w && si.nskip < key_w + 16) {
       // ---- S^T[16 keys x 8*NT heads] = K_w q^T ----
-      float sacc[NT][4];
+      // (two chains of accumulators with one head tile: the products of a chain
+      // wait for one another)
+      constexpr int kChains = NT == 1 ? 2 : 1;
+      float sacc[kChains][NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int ch = 0; ch < kChains; ++ch)
 #pragma unroll
-        for (int f = 0; f < 4; ++f) sacc[nt][f] = 0.f;
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int f = 0; f < 4; ++f) sacc[ch][nt][f] = 0.f;
 #pragma unroll
       for (int up = 0; up < D / 32; ++up) {
         // matrices (keys 0-7 | 8-15) x (16-byte unit u | u+1): lane (g, t)
@@ -485,9 +498,13 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             qa = make_uint2(qf[kk][nt][0], qf[kk][nt][1]);
             qb = make_uint2(qf[kk + 1][nt][0], qf[kk + 1][nt][1]);
           }
-          mma_f16_16816(sacc[nt], k0.x, k1.x, k0.y, k1.y, qa.x, qa.y);
-          mma_f16_16816(sacc[nt], k2.x, k3.x, k2.y, k3.y, qb.x, qb.y);
+          mma_f16_16816(sacc[0][nt], k0.x, k1.x, k0.y, k1.y, qa.x, qa.y);
+          mma_f16_16816(sacc[kChains - 1][nt], k2.x, k3.x, k2.y, k3.y, qb.x, qb.y);
         }
+      }
+      if constexpr (kChains == 2) {
+#pragma unroll
+        for (int f = 0; f < 4; ++f) sacc[0][0][f] += sacc[1][0][f];
       }
       // ---- softmax terms (no sink here) ----
       const uint8_t *sck = smem + C::kScaleOffset + s * C::kScaleBytes + key_w + g8;
@@ -501,10 +518,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       bool grow = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        x[nt][0] = in0 ? sacc[nt][0] * (sl[nt][0] * ks0) : -INFINITY;   // key g,     head 2*tig
-        x[nt][1] = in0 ? sacc[nt][1] * (sl[nt][1] * ks0) : -INFINITY;   // key g,     head 2*tig + 1
-        x[nt][2] = in1 ? sacc[nt][2] * (sl[nt][0] * ks1) : -INFINITY;   // key g + 8, head 2*tig
-        x[nt][3] = in1 ? sacc[nt][3] * (sl[nt][1] * ks1) : -INFINITY;   // key g + 8, head 2*tig + 1
+        x[nt][0] = in0 ? sacc[0][nt][0] * (sl[nt][0] * ks0) : -INFINITY;   // key g,     head 2*tig
+        x[nt][1] = in0 ? sacc[0][nt][1] * (sl[nt][1] * ks0) : -INFINITY;   // key g,     head 2*tig + 1
+        x[nt][2] = in1 ? sacc[0][nt][2] * (sl[nt][0] * ks1) : -INFINITY;   // key g + 8, head 2*tig
+        x[nt][3] = in1 ? sacc[0][nt][3] * (sl[nt][1] * ks1) : -INFINITY;   // key g + 8, head 2*tig + 1
         y[nt][0] = in0 ? x[nt][0] + ev0 : -INFINITY;
         y[nt][1] = in0 ? x[nt][1] + ev0 : -INFINITY;
         y[nt][2] = in1 ? x[nt][2] + ev1 : -INFINITY;
@@ -631,7 +648,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       float *mw = mbuf + warp * 8 * D;
 #pragma unroll
       for (int dm = 0; dm < D / 16; ++dm) {
-        const int d = dm * 16 + 2 * g8;
+        // (the two head pairs of a store's lanes go to different banks)
+        const int d = (dm * 16 + 2 * g8) ^ ((tig & 1) << 4);
         *reinterpret_cast<float2 *>(mw + 2 * tig * D + d) = make_float2(o[dm][nt][0], o[dm][nt][2]);
         *reinterpret_cast<float2 *>(mw + (2 * tig + 1) * D + d) = make_float2(o[dm][nt][1], o[dm][nt][3]);
       }
@@ -656,7 +674,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           const int at = w * NT * 8 + hh;
           den += merge_l[at] * ex2_approx(merge_m[at] - M);
           const float f = ex2_approx(merge_n[at] - M);
-          const float4 v = *reinterpret_cast<const float4 *>(mbuf + (w * 8 + hl) * D + d);
+          const float4 v = *reinterpret_cast<const float4 *>(mbuf + (w * 8 + hl) * D + (d ^ ((hl & 2) << 3)));
           num.x = fmaf(f, v.x, num.x);
           num.y = fmaf(f, v.y, num.y);
           num.z = fmaf(f, v.z, num.z);
