@@ -128,7 +128,10 @@ struct Cfg {
   // Two head tiles at D = 128: the q fragments live in shared memory (per
   // warp), so that twelve warps keep within 128 registers each.
   static constexpr bool kQInSmem = NT == 2 && D >= 128;
-  static constexpr int kTK = 16 * kCW;
+  // 16-key blocks of a warp per tile: two at D = 64, whose rows are half as long
+  // (the same bytes per stage, and two independent chains of work in flight).
+  static constexpr int kKB = D == 64 ? 2 : 1;
+  static constexpr int kTK = 16 * kKB * kCW;
   // Producer warps: each issues the copies of its share of the tile's keys (a
   // warp issues its lanes' TMA copies one after another).
   static constexpr int kPW = 4;
@@ -372,7 +375,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
   // ------------------------------------------------------------- consumers
   const int g8 = lane >> 2;       // key row within an 8-row block of S^T
   const int tig = lane & 3;       // heads 2*tig, 2*tig+1 of a head tile
-  const int key_w = warp * 16;    // this warp's keys within a tile
+  const int key_w = warp * 16 * C::kKB;   // this warp's keys within a tile
   const int bs = p.box_shift;
   // Byte offset of (key row, 16-byte unit u of the row): [box][chunk][row in
   // box][kInner bytes], 128- or 64-byte swizzle.
@@ -382,15 +385,16 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                : static_cast<uint32_t>(krow * C::kInner);
   const uint32_t chunk_stride = 128u << bs;                          // (D = 256)
   const uint32_t swz = D == 64 ? (krow >> 1) & 3 : krow & 7;
-  auto unit_off = [&](int u) -> uint32_t {
+  // (block kb is 16 rows on; D = 256 has one block)
+  auto unit_off = [&](int u, int kb) -> uint32_t {
     if (D == 256) return row_off + (u >> 3) * chunk_stride + (((u & 7) ^ swz) << 4);
-    return row_off + ((u ^ swz) << 4);
+    return row_off + kb * 16 * C::kInner + ((u ^ swz) << 4);
   };
   uint32_t qf[C::kQInSmem ? 1 : D / 16][NT][2];   // B fragments of q^T per k-step and head tile
   uint2 *qsm = reinterpret_cast<uint2 *>(smem + C::kQOffset) + warp * (D / 16) * NT * 32 + lane;
   float o[D / 16][NT][4];                         // O^T accumulators: [d tile][head tile][fragment]
   float sl[NT][2];                                // softmax scale of this lane's heads (with q's power of two)
-  float n_ref[NT][2];                             // numerator reference (one per head, same in every lane)
+  float n_ref[NT][2];                             // numerator reference - headroom (one per head, same in every lane)
   float m_ref[NT][2], l_run[NT][2];               // softmax reference and sum of this lane's keys
   uint32_t merge_phase = 0;
   auto consumers_meet = [&]() -> bool {
@@ -467,84 +471,125 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       if constexpr (C::kQInSmem) __syncwarp();
     }
     // a warp none of whose keys is visible has nothing to add
-    if (si.nvalid > key_w && si.nskip < key_w + 16) {
-      // ---- S^T[16 keys x 8*NT heads] = K_w q^T ----
-      // (two chains of accumulators with one head tile: the products of a chain
-      // wait for one another)
-      constexpr int kChains = NT == 1 ? 2 : 1;
-      float sacc[kChains][NT][4];
+    if (si.nvalid > key_w && si.nskip < key_w + 16 * C::kKB) {
+      // all of the warp's keys visible (the common case): nothing is masked
+      const bool whole = si.nskip <= key_w && si.nvalid >= key_w + 16 * C::kKB;
+      // ---- S^T[16 keys x 8*NT heads] = K_w q^T, per key block ----
+      // (two chains of accumulators where there would be one: the products of a
+      // chain wait for one another)
+      constexpr int KB = C::kKB;
+      constexpr int kChains = NT * KB == 1 ? 2 : 1;
+      float sacc[KB][kChains][NT][4];
 #pragma unroll
-      for (int ch = 0; ch < kChains; ++ch)
+      for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+        for (int ch = 0; ch < kChains; ++ch)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int f = 0; f < 4; ++f) sacc[kb][ch][nt][f] = 0.f;
+#pragma unroll
+      for (int up = 0; up < D / 32; ++up)
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+          // matrices (keys 0-7 | 8-15) x (16-byte unit u | u+1): lane (g, t)
+          // receives d = 16u + 4t .. 4t+3 of keys g and g + 8
+          uint32_t w0, w1, w2, w3;
+          ldmatrix_x4(kbase + unit_off(2 * up + (lane >> 4), kb), w0, w1, w2, w3);
+          const uint2 k0 = e4m3x4_to_f16x2x2(w0), k1 = e4m3x4_to_f16x2x2(w1);
+          const uint2 k2 = e4m3x4_to_f16x2x2(w2), k3 = e4m3x4_to_f16x2x2(w3);
+          const int kk = 2 * up;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            uint2 qa, qb;
+            if constexpr (C::kQInSmem) {
+              qa = qsm[(kk * NT + nt) * 32];
+              qb = qsm[((kk + 1) * NT + nt) * 32];
+            } else {
+              qa = make_uint2(qf[kk][nt][0], qf[kk][nt][1]);
+              qb = make_uint2(qf[kk + 1][nt][0], qf[kk + 1][nt][1]);
+            }
+            mma_f16_16816(sacc[kb][0][nt], k0.x, k1.x, k0.y, k1.y, qa.x, qa.y);
+            mma_f16_16816(sacc[kb][kChains - 1][nt], k2.x, k3.x, k2.y, k3.y, qb.x, qb.y);
+          }
+        }
+      // ---- softmax terms (no sink here) ----
+      // t = S * kscale; the softmax's exponent is t * sl - M, the numerator's t *
+      // sl + ev - m (n_ref is m - headroom): one FMA each.
+      float t[KB][NT][4], ev[KB][2];
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) {
+        const uint8_t *sck = smem + C::kScaleOffset + s * C::kScaleBytes + key_w + kb * 16 + g8;
+        float ks[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const uint32_t b = sck[r * 8], vb = sck[C::kTK + r * 8];
+          ks[r] = scale_value(b);
+          // vb - 127 by way of 2^23 + vb, exact
+          ev[kb][r] = vb == 255u ? NAN : __uint_as_float(0x4B000000u | vb) - 8388735.f;
+        }
+        if constexpr (kChains == 2) {
+#pragma unroll
+          for (int f = 0; f < 4; ++f) sacc[kb][0][0][f] += sacc[kb][1][0][f];
+        }
+        if (!whole) {
+          const int i0 = key_w + kb * 16 + g8;
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            if (i0 + r * 8 < si.nskip || i0 + r * 8 >= si.nvalid) {
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) sacc[kb][0][nt][2 * r] = sacc[kb][0][nt][2 * r + 1] = -INFINITY;
+              ks[r] = 1.f;
+              ev[kb][r] = 0.f;
+            }
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int f = 0; f < 4; ++f) sacc[ch][nt][f] = 0.f;
+          for (int f = 0; f < 4; ++f) t[kb][nt][f] = sacc[kb][0][nt][f] * ks[f >> 1];   // key g + 8*(f>>1), head 2*tig + (f&1)
+      }
+      float zd[KB][NT][4], zn[KB][NT][4];
+      auto exponents = [&]() {
 #pragma unroll
-      for (int up = 0; up < D / 32; ++up) {
-        // matrices (keys 0-7 | 8-15) x (16-byte unit u | u+1): lane (g, t)
-        // receives d = 16u + 4t .. 4t+3 of keys g and g + 8
-        uint32_t w0, w1, w2, w3;
-        ldmatrix_x4(kbase + unit_off(2 * up + (lane >> 4)), w0, w1, w2, w3);
-        const uint2 k0 = e4m3x4_to_f16x2x2(w0), k1 = e4m3x4_to_f16x2x2(w1);
-        const uint2 k2 = e4m3x4_to_f16x2x2(w2), k3 = e4m3x4_to_f16x2x2(w3);
-        const int kk = 2 * up;
+        for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          uint2 qa, qb;
-          if constexpr (C::kQInSmem) {
-            qa = qsm[(kk * NT + nt) * 32];
-            qb = qsm[((kk + 1) * NT + nt) * 32];
-          } else {
-            qa = make_uint2(qf[kk][nt][0], qf[kk][nt][1]);
-            qb = make_uint2(qf[kk + 1][nt][0], qf[kk + 1][nt][1]);
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+              zd[kb][nt][f] = fmaf(t[kb][nt][f], sl[nt][f & 1], -m_ref[nt][f & 1]);
+              zn[kb][nt][f] = fmaf(t[kb][nt][f], sl[nt][f & 1], ev[kb][f >> 1] - n_ref[nt][f & 1]);
+            }
+      };
+      exponents();
+      float top_d = -INFINITY, top_n = -INFINITY;
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int f = 0; f < 4; f += 2) {
+            top_d = fmaxf(top_d, fmaxf(zd[kb][nt][f], zd[kb][nt][f + 1]));
+            top_n = fmaxf(top_n, fmaxf(zn[kb][nt][f], zn[kb][nt][f + 1]));
           }
-          mma_f16_16816(sacc[0][nt], k0.x, k1.x, k0.y, k1.y, qa.x, qa.y);
-          mma_f16_16816(sacc[kChains - 1][nt], k2.x, k3.x, k2.y, k3.y, qb.x, qb.y);
-        }
-      }
-      if constexpr (kChains == 2) {
-#pragma unroll
-        for (int f = 0; f < 4; ++f) sacc[0][0][f] += sacc[1][0][f];
-      }
-      // ---- softmax terms (no sink here) ----
-      const uint8_t *sck = smem + C::kScaleOffset + s * C::kScaleBytes + key_w + g8;
-      const float ks0 = scale_value(sck[0]), ks1 = scale_value(sck[8]);
-      const uint32_t vb0 = sck[C::kTK], vb1 = sck[C::kTK + 8];
-      const float ev0 = vb0 == 255u ? NAN : static_cast<float>(static_cast<int>(vb0) - 127);
-      const float ev1 = vb1 == 255u ? NAN : static_cast<float>(static_cast<int>(vb1) - 127);
-      const int i0 = key_w + g8, i1 = i0 + 8;
-      const bool in0 = i0 >= si.nskip && i0 < si.nvalid, in1 = i1 >= si.nskip && i1 < si.nvalid;
-      float x[NT][4], y[NT][4];
-      bool grow = false;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        x[nt][0] = in0 ? sacc[0][nt][0] * (sl[nt][0] * ks0) : -INFINITY;   // key g,     head 2*tig
-        x[nt][1] = in0 ? sacc[0][nt][1] * (sl[nt][1] * ks0) : -INFINITY;   // key g,     head 2*tig + 1
-        x[nt][2] = in1 ? sacc[0][nt][2] * (sl[nt][0] * ks1) : -INFINITY;   // key g + 8, head 2*tig
-        x[nt][3] = in1 ? sacc[0][nt][3] * (sl[nt][1] * ks1) : -INFINITY;   // key g + 8, head 2*tig + 1
-        y[nt][0] = in0 ? x[nt][0] + ev0 : -INFINITY;
-        y[nt][1] = in0 ? x[nt][1] + ev0 : -INFINITY;
-        y[nt][2] = in1 ? x[nt][2] + ev1 : -INFINITY;
-        y[nt][3] = in1 ? x[nt][3] + ev1 : -INFINITY;
-#pragma unroll
-        for (int f = 0; f < 2; ++f)
-          grow = grow || fmaxf(x[nt][f], x[nt][f + 2]) > m_ref[nt][f] + kLazy ||
-                 fmaxf(y[nt][f], y[nt][f + 2]) > n_ref[nt][f] + kLazy;
-      }
-      if (__any_sync(0xffffffffu, grow)) {
+      if (__any_sync(0xffffffffu, top_d > kLazy || top_n > kLazy + kHeadroom)) {
         // a reference is left behind (always on a piece's first tile, rarely
         // after it): move both up to the maxima seen
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int f = 0; f < 2; ++f) {
-            const float m1 = fmaxf(m_ref[nt][f], fmaxf(x[nt][f], x[nt][f + 2]));
+            float m1 = m_ref[nt][f], n1 = -INFINITY;
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) {
+              const float x0 = t[kb][nt][f] * sl[nt][f], x1 = t[kb][nt][f + 2] * sl[nt][f];
+              m1 = fmaxf(m1, fmaxf(x0, x1));
+              n1 = fmaxf(n1, fmaxf(x0 + ev[kb][0], x1 + ev[kb][1]));
+            }
             l_run[nt][f] *= ex2_approx(m_ref[nt][f] - m1);
             m_ref[nt][f] = m1;
-            float n1 = fmaxf(y[nt][f], y[nt][f + 2]);
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, off));
-            n1 = fmaxf(n_ref[nt][f], n1);
+            n1 = fmaxf(n_ref[nt][f], n1 - kHeadroom);
             const float al = ex2_approx(n_ref[nt][f] - n1);
             n_ref[nt][f] = n1;
 #pragma unroll
@@ -553,17 +598,20 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
               o[dm][nt][f + 2] *= al;
             }
           }
+        exponents();
       }
-      uint32_t pb[NT][2];
+      uint32_t pb[KB][NT][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        l_run[nt][0] += ex2_approx(x[nt][0] - m_ref[nt][0]) + ex2_approx(x[nt][2] - m_ref[nt][0]);
-        l_run[nt][1] += ex2_approx(x[nt][1] - m_ref[nt][1]) + ex2_approx(x[nt][3] - m_ref[nt][1]);
-        const float r0 = n_ref[nt][0] - kHeadroom, r1 = n_ref[nt][1] - kHeadroom;
-        // P^T fragments, transposed into the B operand of O^T += V^T P^T
-        pb[nt][0] = movmatrix_trans(pack_f16x2(ex2_approx(y[nt][0] - r0), ex2_approx(y[nt][1] - r1)));
-        pb[nt][1] = movmatrix_trans(pack_f16x2(ex2_approx(y[nt][2] - r0), ex2_approx(y[nt][3] - r1)));
-      }
+      for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const float *d = zd[kb][nt], *n = zn[kb][nt];
+          l_run[nt][0] += ex2_approx(d[0]) + ex2_approx(d[2]);
+          l_run[nt][1] += ex2_approx(d[1]) + ex2_approx(d[3]);
+          // P^T fragments, transposed into the B operand of O^T += V^T P^T
+          pb[kb][nt][0] = movmatrix_trans(pack_f16x2(ex2_approx(n[0]), ex2_approx(n[1])));
+          pb[kb][nt][1] = movmatrix_trans(pack_f16x2(ex2_approx(n[2]), ex2_approx(n[3])));
+        }
       // ---- O^T[D x 8*NT] += V_w^T P^T ----
       // ldmatrix.trans of bytes taken as 16-bit pairs: lane (g, t) receives
       // keys 2t, 2t+1 (2t+8, 2t+9) at d = 16u + 2g and 2g + 1; one byte permute
@@ -571,39 +619,40 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       // 2g and 16u + 2g + 1.  Codes of keys outside [nskip, nvalid) may be
       // anything (NaN included): on the tiles that have any they are zeroed here.
       auto pv = [&](auto masked) {
-        uint32_t mlo = 0xFFFFFFFFu, mhi = 0xFFFFFFFFu;
-        if constexpr (decltype(masked)::value) {
-          const int ka = key_w + 2 * tig;
-          auto in = [&](int k) { return k >= si.nskip && k < si.nvalid; };
-          mlo = (in(ka) ? 0x0000FFFFu : 0u) | (in(ka + 1) ? 0xFFFF0000u : 0u);
-          mhi = (in(ka + 8) ? 0x0000FFFFu : 0u) | (in(ka + 9) ? 0xFFFF0000u : 0u);
-        }
 #pragma unroll
-        for (int up = 0; up < D / 32; ++up) {
-          uint32_t w0, w1, w2, w3;
-          ldmatrix_x4_trans(vbase + unit_off(2 * up + (lane >> 4)), w0, w1, w2, w3);
-          w0 = __byte_perm(w0, 0u, 0x3120);
-          w1 = __byte_perm(w1, 0u, 0x3120);
-          w2 = __byte_perm(w2, 0u, 0x3120);
-          w3 = __byte_perm(w3, 0u, 0x3120);
+        for (int kb = 0; kb < KB; ++kb) {
+          uint32_t blo = 0xFFFFFFFFu, bhi = 0xFFFFFFFFu;   // bytes: keys k, k+1 of d even, then of d odd
           if constexpr (decltype(masked)::value) {
-            // (bytes: d even of keys k, k+1, then d odd of keys k, k+1)
-            const uint32_t blo = __byte_perm(mlo, 0u, 0x2020), bhi = __byte_perm(mhi, 0u, 0x2020);
-            w0 &= blo;
-            w1 &= bhi;
-            w2 &= blo;
-            w3 &= bhi;
+            const int ka = key_w + kb * 16 + 2 * tig;
+            auto in = [&](int k) { return k >= si.nskip && k < si.nvalid; };
+            blo = (in(ka) ? 0x00FF00FFu : 0u) | (in(ka + 1) ? 0xFF00FF00u : 0u);
+            bhi = (in(ka + 8) ? 0x00FF00FFu : 0u) | (in(ka + 9) ? 0xFF00FF00u : 0u);
           }
-          const uint2 v0 = e4m3x4_to_f16x2x2(w0), v1 = e4m3x4_to_f16x2x2(w1);
-          const uint2 v2 = e4m3x4_to_f16x2x2(w2), v3 = e4m3x4_to_f16x2x2(w3);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma_f16_16816(o[2 * up][nt], v0.x, v0.y, v1.x, v1.y, pb[nt][0], pb[nt][1]);
-            mma_f16_16816(o[2 * up + 1][nt], v2.x, v2.y, v3.x, v3.y, pb[nt][0], pb[nt][1]);
+          for (int up = 0; up < D / 32; ++up) {
+            uint32_t w0, w1, w2, w3;
+            ldmatrix_x4_trans(vbase + unit_off(2 * up + (lane >> 4), kb), w0, w1, w2, w3);
+            w0 = __byte_perm(w0, 0u, 0x3120);
+            w1 = __byte_perm(w1, 0u, 0x3120);
+            w2 = __byte_perm(w2, 0u, 0x3120);
+            w3 = __byte_perm(w3, 0u, 0x3120);
+            if constexpr (decltype(masked)::value) {
+              w0 &= blo;
+              w1 &= bhi;
+              w2 &= blo;
+              w3 &= bhi;
+            }
+            const uint2 v0 = e4m3x4_to_f16x2x2(w0), v1 = e4m3x4_to_f16x2x2(w1);
+            const uint2 v2 = e4m3x4_to_f16x2x2(w2), v3 = e4m3x4_to_f16x2x2(w3);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma_f16_16816(o[2 * up][nt], v0.x, v0.y, v1.x, v1.y, pb[kb][nt][0], pb[kb][nt][1]);
+              mma_f16_16816(o[2 * up + 1][nt], v2.x, v2.y, v3.x, v3.y, pb[kb][nt][0], pb[kb][nt][1]);
+            }
           }
         }
       };
-      if (si.nskip <= key_w && si.nvalid >= key_w + 16)
+      if (whole)
         pv(std::false_type{});
       else
         pv(std::true_type{});
@@ -636,7 +685,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
           const int at = warp * NT * 8 + nt * 8 + 2 * tig + f;
-          merge_n[at] = n_ref[nt][f] - kHeadroom;
+          merge_n[at] = n_ref[nt][f];
           merge_m[at] = m_ref[nt][f];
           merge_l[at] = l_run[nt][f];
         }

@@ -38,7 +38,8 @@ __device__ __forceinline__ float row_inv_scale(int byte) {
 // NaN.  (Bytes outside [10, 246] are never written here, but a pool may hold
 // anything.)
 __device__ __forceinline__ float scale_value(uint32_t byte) {
-  return __uint_as_float(byte == 0u ? 0x00400000u : (byte == 255u ? 0x7FC00000u : byte << 23));
+  const uint32_t odd = byte == 0u ? 0x00400000u : 0x7FC00000u;
+  return __uint_as_float(byte - 1u < 254u ? byte << 23 : odd);
 }
 
 // Two f32 to two e4m3 codes (low byte first), nearest even, saturating; NaN
