@@ -44,6 +44,7 @@
 namespace attnsink {
 namespace {
 
+constexpr uint32_t kBarInit = 1;      // named barrier: every thread, once
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 enum : int { kWhereFull = 401, kWhereEmpty = 402, kWhereMerge = 403 };
@@ -95,6 +96,7 @@ Workspace layout(const PagedFp8Args &a, int teams) {
 struct Params {
   PagedFp8Args a;
   int G, teams, page_shift, box_rows, box_shift;
+  int out8;                              // rows of out keep 8-byte alignment
   float scale_log2;
   int2 *info;
   float *lse_part, *o_part;
@@ -120,13 +122,19 @@ struct StageInfo {
   int nskip, flags, pad0, pad1;        // flags: 1 first tile of a piece, 2 last tile, 4 end of work
 };
 
+// A piece's partial states of one head tile, handed to the producer warps.
+struct MergeUnit {
+  int b, hk, dest, nt;                 // as StageInfo; head tile
+  int stage, last, pad0, pad1;         // the stage that holds O; the piece's last unit
+};
+
 template <int D, int NT>
 struct Cfg {
   // Consumer warps: twelve hide the conversion's latency; at D = 256 eight, as
   // many as three 64 KB stages allow.
   static constexpr int kCW = D == 256 ? 8 : 12;
-  // Two head tiles at D = 128: the q fragments live in shared memory (per
-  // warp), so that twelve warps keep within 128 registers each.
+  // Two head tiles at D = 128: the q fragments stay in shared memory, so that
+  // twelve warps keep within 128 registers each.
   static constexpr bool kQInSmem = NT == 2 && D >= 128;
   // 16-key blocks of a warp per tile: two at D = 64, whose rows are half as long
   // (the same bytes per stage, and two independent chains of work in flight).
@@ -143,26 +151,40 @@ struct Cfg {
   static constexpr int kTileBytes = kTK * D;
   static constexpr int kStageBytes = 2 * kTileBytes;        // K then V
   static constexpr int kScaleBytes = 2 * kTK;               // per stage: K then V
-  static constexpr int kQBytes = kQInSmem ? kCW * (D / 16) * NT * 32 * 8 : 0;
-  static constexpr int kFixed = 1024 /* alignment */ + kQBytes + 2 * kCW * NT * 8 * 8 + 512;
+  // a piece's q as B fragments [k-step][head tile][lane] and its heads' scales;
+  // two slots, so that a piece's is ready before the previous one ends
+  static constexpr int kQSlot = (D / 16) * NT * 32 * 8 + NT * 8 * 4;
+  static constexpr int kQBytes = (2 * kQSlot + 127) / 128 * 128;
+  static constexpr int kFixed = 1024 /* alignment */ + kQBytes + 3 * kCW * 8 * 4 + 1024;
   static constexpr int kStagesRaw = (232448 - kFixed) / (kStageBytes + kScaleBytes + 64);
   static constexpr int kStages = kStagesRaw > 8 ? 8 : kStagesRaw;
   static constexpr int kQOffset = kStages * kStageBytes;
   static constexpr int kScaleOffset = kQOffset + kQBytes;
   static constexpr int kInfoOffset = kScaleOffset + (kStages * kScaleBytes + 127) / 128 * 128;
-  // stage infos and barriers, the merge barrier, (m, M, L) per warp and head,
-  // scan scratch, abort flag
-  static constexpr int kTail = kStages * (32 + 16) + 8 + 3 * kCW * NT * 8 * 4 + 32 * 8 + 32;
+  // stage infos and barriers; the consumers' meeting, merge and q barriers; the
+  // merge unit, (m, M, L) per warp and head, abort flag
+  static constexpr int kTail = kStages * (32 + 16) + 8 * 8 + 32 + 3 * kCW * 8 * 4 + 32;
   static constexpr int kSmemBytes = kInfoOffset + kTail + 1024;
   static_assert(kStages >= 3, "ring");
   static_assert(kSmemBytes <= 232448, "shared-memory budget");
   static_assert(kCW * 8 * D * 4 <= kStageBytes, "one merge pass fits a stage");
+  static_assert(kCW % kPW == 0, "the producer warps arrive for the consumers after a merge");
   static_assert(kShare * kPW * 16 == kTK && kShare <= 16, "one lane per 16 keys of K and of V");
 };
 
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const WaitCtx &ctx, int where) {
   const bool r = mbar_wait(bar, parity, ctx, where);
   return __all_sync(0xffffffffu, r);
+}
+
+__device__ __forceinline__ void mbar_arrive_n(uint64_t *bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
+}
+
+// Quotient of non-negative values, by the 32-bit divider where they fit.
+__device__ __forceinline__ long long div_ll(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
 }
 
 // 16 bytes global -> shared, or 16 zero bytes when !valid (nothing is read).
@@ -192,61 +214,36 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
   StageInfo *info = reinterpret_cast<StageInfo *>(smem + C::kInfoOffset);
   uint64_t *full = reinterpret_cast<uint64_t *>(info + C::kStages);
   uint64_t *empty = full + C::kStages;
-  uint64_t *merge_bar = empty + C::kStages;
-  long long *scan = reinterpret_cast<long long *>(merge_bar + 1);   // [32]
-  float *merge_n = reinterpret_cast<float *>(scan + 32);            // numerator reference [kCW][NT*8]
-  float *merge_m = merge_n + C::kCW * NT * 8;                       // softmax reference
-  float *merge_l = merge_m + C::kCW * NT * 8;                       // softmax sum
-  int *abort_flag = reinterpret_cast<int *>(merge_l + C::kCW * NT * 8);
+  uint64_t *meet = empty + C::kStages;       // the consumers are done with a piece's last stage
+  uint64_t *merge_full = meet + 1;           // a merge unit is in shared memory
+  uint64_t *merge_free = merge_full + 1;     // and has been read
+  uint64_t *q_full = merge_free + 1;         // [2] a piece's q is in its slot
+  uint64_t *q_free = q_full + 2;             // [2] and is no longer needed
+  MergeUnit *unit = reinterpret_cast<MergeUnit *>(q_free + 3);
+  float *merge_n = reinterpret_cast<float *>(unit + 1);             // numerator reference [kCW][8]
+  float *merge_m = merge_n + C::kCW * 8;                            // softmax reference
+  float *merge_l = merge_m + C::kCW * 8;                            // softmax sum
+  int *abort_flag = reinterpret_cast<int *>(merge_l + C::kCW * 8);
   const PagedFp8Args &a = p.a;
   const WaitCtx ctx{abort_flag, a.status, wait_limit_ns(a.status)};
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
-  // ------------------------------------------------------------------ plan
-  // Thread t counts the tiles of a run of sequences; a block-wide scan gives
-  // every run's first tile and the total.
-  const int per = (a.B + C::kThreads - 1) / C::kThreads;
-  const int run0 = min(a.B, static_cast<int>(threadIdx.x) * per), run1 = min(a.B, run0 + per);
-  long long mine = 0;
-  for (int b = run0; b < run1; ++b) mine += range_of<C::kTK>(p, a.seqlens[b]).tiles;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1 + 32 * C::kPW);   // one expect_tx, and every producer lane's scale copies
       mbar_init(&empty[s], C::kCW);
     }
-    mbar_init(merge_bar, C::kCW * 32);
+    mbar_init(meet, C::kCW);
+    mbar_init(merge_full, C::kCW);
+    mbar_init(merge_free, C::kPW);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_free[i], C::kCW);
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
-  long long incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
-  }
-  if (lane == 31) scan[warp] = incl;
-  __syncthreads();
-  long long before = incl - mine, total = 0;
-#pragma unroll
-  for (int w = 0; w < C::kWarps; ++w) {
-    const long long s = scan[w];
-    if (w < warp) before += s;
-    total += s;
-  }
-  const int E = static_cast<int>(min(static_cast<long long>(p.teams), total));   // spans in use
-  const int items = E * a.Hkv;
-  if (blockIdx.x == 0 && threadIdx.x == 0) p.info[p.teams] = make_int2(E, 0);
-  if (static_cast<int>(blockIdx.x) >= items) return;
-  auto span_start = [&](int j) { return static_cast<long long>(j) * total / E; };
-  // the run that holds the first tile of this CTA's first span
-  const long long first_tile = span_start(blockIdx.x / a.Hkv);
-  __syncthreads();                     // (every thread has read scan[])
-  if (mine > 0 && before <= first_tile && first_tile < before + mine) {
-    scan[0] = before;
-    scan[1] = run0;
-  }
-  __syncthreads();
 
   if (warp >= C::kCW) {
     // ------------------------------------------------------------- producers
@@ -259,31 +256,195 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       tma_prefetch_desc(&tmK);
       tma_prefetch_desc(&tmV);
     }
+    // ---- plan: every producer warp finds the CTA's share for itself (the
+    // consumers need none of it).  Lane l counts the tiles of a run of sequences;
+    // a scan over the warp gives every run's first tile and the total.
+    const int per = (a.B + 31) / 32;
+    const int run0 = min(a.B, lane * per), run1 = min(a.B, run0 + per);
+    long long mine = 0;
+#pragma unroll 4
+    for (int b = run0; b < run1; ++b) mine += range_of<C::kTK>(p, a.seqlens[b]).tiles;
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const long long total = __shfl_sync(0xffffffffu, incl, 31);
+    const int E = static_cast<int>(min(static_cast<long long>(p.teams), total));   // spans in use
+    const int items = E * a.Hkv;
+    if (blockIdx.x == 0 && lead) p.info[p.teams] = make_int2(E, 0);
+    // spans of q + 1 tiles, rem of them, then of q
+    const long long span = E > 0 ? div_ll(total, E) : 0;
+    const long long rem = E > 0 ? total - span * E : 0;
+    auto span_start = [&](int j) { return j * span + min(static_cast<long long>(j), rem); };
+    // the first sequence of this CTA's first span, and its first tile
+    int b_from = 0;
+    long long base_from = 0;
+    if (static_cast<int>(blockIdx.x) < items) {
+      const long long first_tile = span_start(blockIdx.x / a.Hkv);
+      const uint32_t owner = __ballot_sync(0xffffffffu, incl - mine <= first_tile && first_tile < incl);
+      const int src = __ffs(owner) - 1;
+      b_from = __shfl_sync(0xffffffffu, run0, src);
+      base_from = __shfl_sync(0xffffffffu, incl - mine, src);
+    }
+    named_barrier_sync(kBarInit, C::kThreads);      // the barriers are initialised
     const int kv = lane >> 4, c = pw * C::kShare + (lane & 15);
     const int rows = p.box_rows;
     const bool active = (lane & 15) < C::kShare;
     const bool issues = active && (c * 16) % rows == 0;   // this lane's 16 keys start a box
     const uint8_t *scales = kv ? a.vscales : a.kscales;
     const int64_t sc_page = kv ? a.vs_s[0] : a.ks_s[0], sc_head = kv ? a.vs_s[1] : a.ks_s[1];
-    int slot = 0;
+    int slot = 0, pieces = 0, merged = 0;
     bool ok = true;
+    // ---- merge units: the consumers leave a piece's partial states in its last
+    // stage and go on; every producer warp takes a share of the outputs ----
+    auto merge = [&]() {
+      const MergeUnit u = *unit;
+      const float *mbuf = reinterpret_cast<const float *>(smem + u.stage * C::kStageBytes);   // [warp][8 heads][D]
+      const int heads = min(p.G - u.nt * 8, 8);
+      for (int e = pw * 32 + lane; e < heads * (D / 4); e += C::kPW * 32) {
+        const int hl = e / (D / 4), d = (e - hl * (D / 4)) * 4;
+        const int hq = u.hk * p.G + u.nt * 8 + hl;
+        float M = kNoMax;
+#pragma unroll
+        for (int w = 0; w < C::kCW; ++w) M = fmaxf(M, merge_m[w * 8 + hl]);
+        // the sink joins here if no other span holds keys of this sequence
+        float den = 0.f;
+        if (u.dest < 0) {
+          const float sink2 = a.sinks[hq] * kLog2e;
+          M = fmaxf(M, sink2);
+          den = ex2_approx(sink2 - M);
+        }
+        float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < C::kCW; ++w) {
+          den += merge_l[w * 8 + hl] * ex2_approx(merge_m[w * 8 + hl] - M);
+          const float f = ex2_approx(merge_n[w * 8 + hl] - M);
+          const float4 v = *reinterpret_cast<const float4 *>(mbuf + (w * 8 + hl) * D + (d ^ (hl >> 1 << 3)));
+          num.x = fmaf(f, v.x, num.x);
+          num.y = fmaf(f, v.y, num.y);
+          num.z = fmaf(f, v.z, num.z);
+          num.w = fmaf(f, v.w, num.w);
+        }
+        const float inv = den != 0.f ? 1.f / den : 0.f;
+        num = make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
+        if (u.dest < 0) {
+          __nv_bfloat16 *po = a.out + u.b * a.o_s[0] + hq * a.o_s[1] + d;
+          if (p.out8) {
+            *reinterpret_cast<uint2 *>(po) = make_uint2(pack_bf16x2(num.x, num.y), pack_bf16x2(num.z, num.w));
+          } else {
+            po[0] = __float2bfloat16_rn(num.x);
+            po[1] = __float2bfloat16_rn(num.y);
+            po[2] = __float2bfloat16_rn(num.z);
+            po[3] = __float2bfloat16_rn(num.w);
+          }
+        } else {
+          const size_t row = static_cast<size_t>(u.dest) * a.Hq + hq;
+          *reinterpret_cast<float4 *>(p.o_part + row * D + d) = num;
+          if (d == 0) p.lse_part[row] = (M + log2f(den)) * kLn2;
+        }
+      }
+      // the generic reads are ordered before the next TMA write into the stage
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(merge_free);
+        if (u.last) mbar_arrive_n(&empty[u.stage], C::kCW / C::kPW);
+      }
+      ++merged;
+    };
+    // Merges the next unit if it is there; all lanes agree.
+    auto poll_merge = [&]() -> bool {
+      bool there = false;
+      if (lane == 0) there = mbar_try_wait(merge_full, static_cast<uint32_t>(merged) & 1u);
+      if (!__shfl_sync(0xffffffffu, there, 0)) return false;
+      __syncwarp();
+      merge();
+      return true;
+    };
+    // Bounded wait for `bar`, merging units meanwhile (the stage that is waited
+    // for may be one that a unit holds).
+    auto wait_or_merge = [&](uint64_t *bar, uint32_t parity, int where) -> bool {
+      uint64_t w0 = 0;
+      for (;;) {
+        int st = 0;                    // 1 there, 2 given up
+        if (lane == 0) {
+          if (ctx.limit >= kWaitSleepNs && mbar_try_wait(bar, parity)) st = 1;
+          else if (w0 == 0) w0 = globaltimer_ns();
+          else if (mbar_try_wait_sleep(bar, parity, ctx.limit < 1000 ? static_cast<uint32_t>(ctx.limit) : 1000u)) st = 1;
+          else if (*ctx.abort) st = 2;
+          else if (globaltimer_ns() - w0 > ctx.limit) {
+            report_timeout(ctx.status, where);
+            *ctx.abort = 1;
+            st = 2;
+          }
+        }
+        st = __shfl_sync(0xffffffffu, st, 0);
+        if (st == 1) return true;
+        if (st == 2) return false;
+        if (poll_merge()) w0 = 0;
+      }
+    };
     auto acquire = [&]() -> int {
       const int s = slot % C::kStages;
       const uint32_t use = static_cast<uint32_t>(slot / C::kStages);
-      bool good = true;
-      if (lane == 0 && slot >= C::kStages && !mbar_wait(&empty[s], (use & 1u) ^ 1u, ctx, kWhereEmpty)) good = false;
-      ok = ok && __shfl_sync(0xffffffffu, good, 0);
+      ok = ok && (slot < C::kStages || wait_or_merge(&empty[s], (use & 1u) ^ 1u, kWhereEmpty));
       if (ok) ++slot;
       return s;
     };
+    // The last producer warp prepares a piece's q: f16 under a power of two per
+    // head that puts its largest magnitude in [2^13, 2^14) (exact for elements
+    // above max * 2^-27); k = 2t, 2t+1, 2t+8, 2t+9 of a k-step hold d = 4t .. 4t+3
+    // of its 16, the order K's bytes arrive in.
+    auto prepare_q = [&](int b, int hk) {
+      const int qs = pieces & 1;
+      if (pieces >= 2) ok = ok && wait_or_merge(&q_free[qs], static_cast<uint32_t>((pieces >> 1) - 1) & 1u, kWhereEmpty);
+      if (!ok) return;
+      uint2 *qsm = reinterpret_cast<uint2 *>(smem + C::kQOffset + qs * C::kQSlot) + lane;
+      float *qscale = reinterpret_cast<float *>(smem + C::kQOffset + qs * C::kQSlot + (D / 16) * NT * 32 * 8);
+      const int g8 = lane >> 2, tig = lane & 3;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        uint32_t x[D / 16][2];
+        const int hl = nt * 8 + g8;
+        const __nv_bfloat16 *qr = a.q + b * a.q_s[0] + (hk * p.G + hl) * a.q_s[1] + 4 * tig;
+        float mx = 0.f;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          x[kk][0] = x[kk][1] = 0u;
+          if (hl < p.G) {
+            x[kk][0] = *reinterpret_cast<const uint32_t *>(qr + kk * 16);
+            x[kk][1] = *reinterpret_cast<const uint32_t *>(qr + kk * 16 + 2);
+          }
+        }
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+          for (int f = 0; f < 2; ++f)
+            mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(x[kk][f] << 16)), fabsf(__uint_as_float(x[kk][f] & 0xFFFF0000u))));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        int e = 0;
+        // (at most 2^126, so that the scale itself stays finite: a smaller q
+        // only lies lower in f16's range)
+        if (mx > 0.f && mx < INFINITY) e = min(13 - ilogbf(mx), 126);
+        const float sc = ldexpf(1.f, e);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          qsm[(kk * NT + nt) * 32] = make_uint2(f32x2_to_f16x2(x[kk][0], sc), f32x2_to_f16x2(x[kk][1], sc));
+        if (tig == 0) qscale[nt * 8 + g8] = ldexpf(p.scale_log2, -e);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[qs]);
+    };
     // (b, base): a sequence and its first tile; items come in the spans' order,
     // and the walk of one begins where its span does
-    int b_from = static_cast<int>(scan[1]);
-    long long base_from = scan[0];
     for (int item = blockIdx.x; ok && item < items; item += gridDim.x) {
       const int team = item / a.Hkv, hk = item - team * a.Hkv;
       const long long t0 = span_start(team), t1 = span_start(team + 1);
       int2 note = make_int2(-1, 0);    // the sequence that begins in this span and is cut by its end
+      long long last_tile = 0;         // and its last tile
       int b = b_from;
       long long base = base_from;
       Range r = range_of<C::kTK>(p, a.seqlens[b]);
@@ -301,8 +462,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         const int i1 = static_cast<int>(min(static_cast<long long>(r.tiles), t1 - base));
         const bool whole = i0 == 0 && i1 == r.tiles;
         const int dest = whole ? -1 : 2 * team + (i0 == 0 ? 1 : 0);
-        if (i0 == 0 && i1 < r.tiles)
-          note = make_int2(b, static_cast<int>(((base + r.tiles) * E - 1) / total));   // the span of its last tile
+        if (i0 == 0 && i1 < r.tiles) {
+          note.x = b;
+          last_tile = base + r.tiles - 1;
+        }
         const int *table = a.block_table + static_cast<int64_t>(b) * a.bt_s0;
         auto page_of = [&](int i) -> int {   // pool page of this lane's 16 keys of tile i
           const int key = r.start + i * C::kTK + c * 16;
@@ -343,10 +506,20 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             copy16_async(smem + C::kScaleOffset + s * C::kScaleBytes + kv * C::kTK + c * 16,
                          scales + (pg < 0 ? 0 : pg * sc_page + hk * sc_head + at), pg >= 0);
           copy_async_arrive(&full[s]);
+          if (i == i0) {
+            if (pw == C::kPW - 1) prepare_q(b, hk);
+            ++pieces;
+          }
+          poll_merge();
         }
         t = base + i1;
       }
-      if (hk == 0 && lead) p.info[team] = note;
+      if (hk == 0 && lead) {
+        const long long wide = rem * (span + 1);    // tiles of the longer spans
+        if (note.x >= 0)
+          note.y = static_cast<int>(last_tile < wide ? div_ll(last_tile, span + 1) : rem + div_ll(last_tile - wide, span));
+        p.info[team] = note;
+      }
     }
     if (ok) {
       const int s = acquire();
@@ -359,6 +532,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         copy_async_arrive(&full[s]);
       }
     }
+    // the units still to come (the last one's stage stays taken: its consumers
+    // are done with the ring)
+    while (ok && merged < pieces * NT) ok = wait_or_merge(merge_full, static_cast<uint32_t>(merged) & 1u, kWhereMerge) && (poll_merge(), true);
     // Every copy has landed before this warp leaves: the CTA's shared memory
     // outlives them, also when the consumers gave up early (each wait is bounded
     // by the fixed limit, whatever limit the other waits use).
@@ -372,6 +548,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     return;
   }
 
+  named_barrier_sync(kBarInit, C::kThreads);
   // ------------------------------------------------------------- consumers
   const int g8 = lane >> 2;       // key row within an 8-row block of S^T
   const int tig = lane & 3;       // heads 2*tig, 2*tig+1 of a head tile
@@ -391,18 +568,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     return row_off + kb * 16 * C::kInner + ((u ^ swz) << 4);
   };
   uint32_t qf[C::kQInSmem ? 1 : D / 16][NT][2];   // B fragments of q^T per k-step and head tile
-  uint2 *qsm = reinterpret_cast<uint2 *>(smem + C::kQOffset) + warp * (D / 16) * NT * 32 + lane;
+  const uint2 *qsm = nullptr;                     // or where they are (this lane's)
   float o[D / 16][NT][4];                         // O^T accumulators: [d tile][head tile][fragment]
   float sl[NT][2];                                // softmax scale of this lane's heads (with q's power of two)
   float n_ref[NT][2];                             // numerator reference - headroom (one per head, same in every lane)
   float m_ref[NT][2], l_run[NT][2];               // softmax reference and sum of this lane's keys
-  uint32_t merge_phase = 0;
-  auto consumers_meet = [&]() -> bool {
-    mbar_arrive(merge_bar);
-    const bool met = warp_wait(merge_bar, merge_phase & 1u, ctx, kWhereMerge);
-    ++merge_phase;
-    return met;
-  };
+  int piece = -1, units = 0;
   for (int slot = 0;; ++slot) {
     const int s = slot % C::kStages;
     if (!warp_wait(&full[s], static_cast<uint32_t>(slot / C::kStages) & 1u, ctx, kWhereFull)) break;
@@ -411,56 +582,34 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     const uint32_t kbase = smem_u32(smem + s * C::kStageBytes);
     const uint32_t vbase = kbase + C::kTileBytes;
     if (si.flags & 1) {
-      // a piece begins: the grouped queries of this kv head, in f16 under a
-      // power of two per head that puts its largest magnitude in [2^13, 2^14)
-      // (exact for elements above max * 2^-27); k = 2t, 2t+1, 2t+8, 2t+9 of a
-      // k-step hold d = 4t .. 4t+3 of its 16, the order K's bytes arrive in
+      // a piece begins: its queries
+      ++piece;
+      const int qs = piece & 1;
+      if (!warp_wait(&q_full[qs], static_cast<uint32_t>(piece >> 1) & 1u, ctx, kWhereFull)) break;
+      const uint8_t *slot_q = smem + C::kQOffset + qs * C::kQSlot;
+      qsm = reinterpret_cast<const uint2 *>(slot_q) + lane;
+      const float *qscale = reinterpret_cast<const float *>(slot_q + (D / 16) * NT * 32 * 8);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        uint32_t x[D / 16][2];
-        const int hl = nt * 8 + g8;
-        const __nv_bfloat16 *qr = a.q + si.b * a.q_s[0] + (si.hk * p.G + hl) * a.q_s[1] + 4 * tig;
-        float mx = 0.f;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          x[kk][0] = x[kk][1] = 0u;
-          if (hl < p.G) {
-            x[kk][0] = *reinterpret_cast<const uint32_t *>(qr + kk * 16);
-            x[kk][1] = *reinterpret_cast<const uint32_t *>(qr + kk * 16 + 2);
-          }
-        }
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-#pragma unroll
-          for (int f = 0; f < 2; ++f)
-            mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(x[kk][f] << 16)), fabsf(__uint_as_float(x[kk][f] & 0xFFFF0000u))));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        int e = 0;
-        // (at most 2^126, so that the scale itself stays finite: a smaller q
-        // only lies lower in f16's range)
-        if (mx > 0.f && mx < INFINITY) e = min(13 - ilogbf(mx), 126);
-        const float qs = ldexpf(1.f, e);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t q0 = f32x2_to_f16x2(x[kk][0], qs), q1 = f32x2_to_f16x2(x[kk][1], qs);
-          if constexpr (C::kQInSmem) {
-            qsm[(kk * NT + nt) * 32] = make_uint2(q0, q1);
-          } else {
-            qf[kk][nt][0] = q0;
-            qf[kk][nt][1] = q1;
-          }
-        }
-        // the lanes of head h (8 columns) are 4h .. 4h+3; this lane's S columns
-        // are heads 2*tig and 2*tig + 1
-        const float ms = ldexpf(p.scale_log2, -e);
-        sl[nt][0] = __shfl_sync(0xffffffffu, ms, 8 * tig);
-        sl[nt][1] = __shfl_sync(0xffffffffu, ms, 8 * tig + 4);
+        sl[nt][0] = qscale[nt * 8 + 2 * tig];
+        sl[nt][1] = qscale[nt * 8 + 2 * tig + 1];
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
           n_ref[nt][f] = m_ref[nt][f] = kNoMax;
           l_run[nt][f] = 0.f;
         }
+        if constexpr (!C::kQInSmem) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint2 f = qsm[(kk * NT + nt) * 32];
+            qf[kk][nt][0] = f.x;
+            qf[kk][nt][1] = f.y;
+          }
+        }
+      }
+      if constexpr (!C::kQInSmem) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_free[qs]);
       }
 #pragma unroll
       for (int dm = 0; dm < D / 16; ++dm)
@@ -468,7 +617,6 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int f = 0; f < 4; ++f) o[dm][nt][f] = 0.f;
-      if constexpr (C::kQInSmem) __syncwarp();
     }
     // a warp none of whose keys is visible has nothing to add
     if (si.nvalid > key_w && si.nskip < key_w + 16 * C::kKB) {
@@ -664,7 +812,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       if (lane == 0) mbar_arrive(&empty[s]);
       continue;
     }
-    // ---- a piece ends: merge the warps' states, write O or (O_s, LSE_s) ----
+    // ---- a piece ends: leave the warp's state in the stage ----
+    if constexpr (C::kQInSmem) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_free[piece & 1]);
+    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -678,77 +830,43 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         m_ref[nt][f] = M;
         l_run[nt][f] = L;
       }
-    if (!consumers_meet()) return;     // every warp is done with this stage
-    if (g8 == 0) {
+    // every warp is done with this stage
+    __syncwarp();
+    if (lane == 0) mbar_arrive(meet);
+    if (!warp_wait(meet, static_cast<uint32_t>(piece) & 1u, ctx, kWhereMerge)) break;
+    float *mw = reinterpret_cast<float *>(smem + s * C::kStageBytes) + warp * 8 * D;   // [warp][8 heads][D]
+    bool left = false;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
+      // the previous unit has been read
+      if (units > 0 && !warp_wait(merge_free, static_cast<uint32_t>(units - 1) & 1u, ctx, kWhereMerge)) {
+        left = true;
+        break;
+      }
+      if (g8 == 0) {
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
-          const int at = warp * NT * 8 + nt * 8 + 2 * tig + f;
+          const int at = warp * 8 + 2 * tig + f;
           merge_n[at] = n_ref[nt][f];
           merge_m[at] = m_ref[nt][f];
           merge_l[at] = l_run[nt][f];
         }
-    }
-    float *mbuf = reinterpret_cast<float *>(smem + s * C::kStageBytes);   // [warp][8 heads][D]
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      if (nt > 0 && !consumers_meet()) return;     // the previous pass is fully read
-      float *mw = mbuf + warp * 8 * D;
+      }
 #pragma unroll
       for (int dm = 0; dm < D / 16; ++dm) {
-        // (the two head pairs of a store's lanes go to different banks)
-        const int d = (dm * 16 + 2 * g8) ^ ((tig & 1) << 4);
+        // (the head pairs of a store's lanes go to different banks)
+        const int d = (dm * 16 + 2 * g8) ^ (tig << 3);
         *reinterpret_cast<float2 *>(mw + 2 * tig * D + d) = make_float2(o[dm][nt][0], o[dm][nt][2]);
         *reinterpret_cast<float2 *>(mw + (2 * tig + 1) * D + d) = make_float2(o[dm][nt][1], o[dm][nt][3]);
       }
-      if (!consumers_meet()) return;
-      const int heads = min(p.G - nt * 8, 8);
-      for (int e = threadIdx.x; e < heads * (D / 4); e += C::kCW * 32) {
-        const int hl = e / (D / 4), d = (e - hl * (D / 4)) * 4, hh = nt * 8 + hl;
-        const int hq = si.hk * p.G + hh;
-        float M = kNoMax;
-#pragma unroll
-        for (int w = 0; w < C::kCW; ++w) M = fmaxf(M, merge_m[w * NT * 8 + hh]);
-        // the sink joins here if no other span holds keys of this sequence
-        float sink2 = -INFINITY;
-        if (si.dest < 0) {
-          sink2 = a.sinks[hq] * kLog2e;
-          M = fmaxf(M, sink2);
-        }
-        float den = si.dest < 0 ? ex2_approx(sink2 - M) : 0.f;
-        float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < C::kCW; ++w) {
-          const int at = w * NT * 8 + hh;
-          den += merge_l[at] * ex2_approx(merge_m[at] - M);
-          const float f = ex2_approx(merge_n[at] - M);
-          const float4 v = *reinterpret_cast<const float4 *>(mbuf + (w * 8 + hl) * D + (d ^ ((hl & 2) << 3)));
-          num.x = fmaf(f, v.x, num.x);
-          num.y = fmaf(f, v.y, num.y);
-          num.z = fmaf(f, v.z, num.z);
-          num.w = fmaf(f, v.w, num.w);
-        }
-        const float inv = den != 0.f ? 1.f / den : 0.f;
-        num = make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
-        if (si.dest < 0) {
-          __nv_bfloat16 *po = a.out + si.b * a.o_s[0] + hq * a.o_s[1] + d;
-          po[0] = __float2bfloat16_rn(num.x);
-          po[1] = __float2bfloat16_rn(num.y);
-          po[2] = __float2bfloat16_rn(num.z);
-          po[3] = __float2bfloat16_rn(num.w);
-        } else {
-          const size_t row = static_cast<size_t>(si.dest) * a.Hq + hq;
-          *reinterpret_cast<float4 *>(p.o_part + row * D + d) = num;
-          if (d == 0) p.lse_part[row] = (M + log2f(den)) * kLn2;
-        }
-      }
+      if (warp == 0 && lane == 0) *unit = MergeUnit{si.b, si.hk, si.dest, nt, s, nt == NT - 1, 0, 0};
+      // (ordered before the next TMA write into the stage)
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(merge_full);
+      ++units;
     }
-    // the merge's generic accesses are ordered before the next TMA write
-    if (!consumers_meet()) return;
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&empty[s]);
+    if (left) break;
   }
 }
 
@@ -757,7 +875,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
 // 32 sequences to write the rows of the empty ones.
 template <int D>
 __global__ void __launch_bounds__(128) paged_fp8_combine_kernel(const __grid_constant__ Params p) {
-  constexpr int kPer = D / 32;                      // channels per lane
+  constexpr int kPer = D / 32;                      // channels per lane, consecutive
+  constexpr int kAhead = 4;                         // parts whose loads do not wait for the weights
   const PagedFp8Args &a = p.a;
   const int lane = threadIdx.x & 31;
   const long long w = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
@@ -774,17 +893,26 @@ __global__ void __launch_bounds__(128) paged_fp8_combine_kernel(const __grid_con
     }
     return;
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int team = static_cast<int>(w / a.Hq), hq = static_cast<int>(w - static_cast<long long>(team) * a.Hq);
-  const int E = min(p.info[p.teams].x, p.teams);
-  if (team >= E) return;
-  // (checked whole: a split whose waits ran out may not have written its note)
+  const float sink = a.sinks[hq];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int2 note = p.info[team];
-  if (note.x < 0 || note.x >= a.B || note.y <= team || note.y >= E) return;
+  const int E = min(p.info[p.teams].x, p.teams);
+  // (checked whole: a split whose waits ran out may not have written its note)
+  if (team >= E || note.x < 0 || note.x >= a.B || note.y <= team || note.y >= E) return;
   const int parts = note.y - team + 1;
   // part 0 is the span's own last piece, part i the first piece of span team + i
   auto slot_of = [&](int i) { return static_cast<size_t>(i == 0 ? 2 * team + 1 : 2 * (team + i)) * a.Hq + hq; };
-  const float sink = a.sinks[hq];
+  float ahead[kAhead][kPer];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+    for (int t = 0; t < kPer; t += 2) {
+      const float2 v = i < parts ? *reinterpret_cast<const float2 *>(p.o_part + slot_of(i) * D + lane * kPer + t)
+                                 : make_float2(0.f, 0.f);
+      ahead[i][t] = v.x;
+      ahead[i][t + 1] = v.y;
+    }
   float M = sink;
   for (int i0 = 0; i0 < parts; i0 += 32) {
     float ls = i0 + lane < parts ? p.lse_part[slot_of(i0 + lane)] : -INFINITY;
@@ -804,18 +932,27 @@ __global__ void __launch_bounds__(128) paged_fp8_combine_kernel(const __grid_con
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
     den += sum;
     const int cnt = min(32, parts - i0);
-#pragma unroll 4
-    for (int i = 0; i < cnt; ++i) {              // spans in order
-      const float ws = __shfl_sync(0xffffffffu, wt, i);
-      const float *op = p.o_part + slot_of(i0 + i) * D + lane;
+    int i = 0;
+    if (i0 == 0) {
 #pragma unroll
-      for (int t = 0; t < kPer; ++t) acc[t] = fmaf(ws, op[32 * t], acc[t]);
+      for (; i < kAhead; ++i) {                  // spans in order
+        const float ws = __shfl_sync(0xffffffffu, wt, i);
+#pragma unroll
+        for (int t = 0; t < kPer; ++t) acc[t] = fmaf(ws, ahead[i][t], acc[t]);
+      }
+    }
+#pragma unroll 4
+    for (; i < cnt; ++i) {
+      const float ws = __shfl_sync(0xffffffffu, wt, i);
+      const float *op = p.o_part + slot_of(i0 + i) * D + lane * kPer;
+#pragma unroll
+      for (int t = 0; t < kPer; ++t) acc[t] = fmaf(ws, op[t], acc[t]);
     }
   }
   const float inv = den != 0.f ? 1.f / den : 0.f;
-  __nv_bfloat16 *po = a.out + static_cast<int64_t>(note.x) * a.o_s[0] + hq * a.o_s[1] + lane;
+  __nv_bfloat16 *po = a.out + static_cast<int64_t>(note.x) * a.o_s[0] + hq * a.o_s[1] + lane * kPer;
 #pragma unroll
-  for (int t = 0; t < kPer; ++t) po[32 * t] = __float2bfloat16_rn(acc[t] * inv);
+  for (int t = 0; t < kPer; ++t) po[t] = __float2bfloat16_rn(acc[t] * inv);
 }
 
 template <int D, int NT>
@@ -858,6 +995,7 @@ cudaError_t launch_decode_paged_fp8(const PagedFp8Args &a, void *workspace, int 
   while ((1 << p.page_shift) < a.page) ++p.page_shift;
   p.box_rows = a.page < 64 ? a.page : 64;
   p.box_shift = p.page_shift < 6 ? p.page_shift : 6;
+  p.out8 = (reinterpret_cast<uintptr_t>(a.out) | (a.o_s[0] * 2) | (a.o_s[1] * 2)) % 8 == 0;
   p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
   const Workspace w = layout(a, p.teams);
   uint8_t *ws = static_cast<uint8_t *>(workspace);
