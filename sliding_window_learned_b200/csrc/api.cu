@@ -359,7 +359,7 @@ static void tma_cache_put(const TmaKey &key, const CUtensorMap &map) {
 }
 
 cudaError_t make_tma_bshd(void *map_out, const void *base, int64_t d3, int64_t d2, int64_t d1,
-                          int64_t d0, const int64_t strides_el[3], int box_rows, int elem_bytes) {
+                          int64_t d0, const int64_t strides_el[3], int box_rows, int elem_bytes, int box_heads) {
   const tma_encode_fn encode = tma_encode();
   if (!encode) return cudaErrorNotSupported;
   TmaKey key;
@@ -371,7 +371,7 @@ cudaError_t make_tma_bshd(void *map_out, const void *base, int64_t d3, int64_t d
   key.s[0] = strides_el[0];
   key.s[1] = strides_el[1];
   key.s[2] = strides_el[2];
-  key.box = box_rows;
+  key.box = box_rows + box_heads * 65536;
   key.elem = elem_bytes;
   if (tma_cache_get(key, map_out)) return cudaSuccess;
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d0), static_cast<cuuint64_t>(d1),
@@ -385,8 +385,8 @@ cudaError_t make_tma_bshd(void *map_out, const void *base, int64_t d3, int64_t d
   // f32 map instead spans the whole row, unswizzled
   const bool f32 = elem_bytes == 4;
   if (f32 && (d0 > 256 || (d0 * 4) % 16 != 0)) return cudaErrorInvalidValue;
-  const cuuint32_t box[4] = {static_cast<cuuint32_t>(f32 ? d0 : 128 / elem_bytes), 1,
-                             static_cast<cuuint32_t>(box_rows), 1};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(f32 ? d0 : 128 / elem_bytes),
+                             static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows), 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   alignas(64) CUtensorMap map;
   const CUtensorMapDataType dt = elem_bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8

@@ -246,8 +246,9 @@ int attn_sink_fwd_extend(const attn_tensor *q, const attn_tensor *k, const attn_
     return fail(ATTN_EUNSUPPORTED, "B and Hq must be <= 65535, T and Tk <= 2^30");
   // no chunk is longer than T
   const int64_t rows = max_seqlen_q < T ? max_seqlen_q : T;
-  if ((rows + 127) / 128 * B * Hq > 0x7FFFFFFF)
-    return fail(ATTN_EUNSUPPORTED, "ceil(max_seqlen_q / 128) * B * Hq must be < 2^31");
+  // query tiles hold at least 112 rows (position, head) each, but for a sequence's last
+  if ((rows * Hq / 112 + Hq) * B > 0x7FFFFFFF)
+    return fail(ATTN_EUNSUPPORTED, "(max_seqlen_q / 112 + 1) * Hq * B must be < 2^31");
   if (B == 0 || rows == 0) return ATTN_OK;
   FwdArgs a;
   a.q = q->data;
@@ -278,8 +279,23 @@ int attn_sink_fwd_extend(const attn_tensor *q, const attn_tensor *k, const attn_
   a.lse_s[0] = 0;
   a.lse_s[1] = lse ? lse->stride[0] : 0;
   if ((rc = status_ptr(&a.status))) return rc;
-  const cudaError_t e = launch_fwd_tc(a, static_cast<cudaStream_t>(stream));
-  return e == cudaSuccess ? ATTN_OK : fail_cuda(e, "attn_sink_fwd_extend launch");
+  if ((rc = sm_count(&a.sms))) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const size_t bytes = fwd_extend_workspace_bytes(a);
+  if (bytes == 0) {
+    const cudaError_t e = launch_fwd_tc(a, st);
+    return e == cudaSuccess ? ATTN_OK : fail_cuda(e, "attn_sink_fwd_extend launch");
+  }
+  cudaMemPool_t pool;
+  if ((rc = workspace_pool(&pool))) return rc;
+  if (take_injected_alloc_failure()) return fail(ATTN_ENOMEM, "extend workspace allocation failed (injected)");
+  cudaError_t e = cudaMallocFromPoolAsync(&a.workspace, bytes, pool, st);
+  if (e != cudaSuccess) return fail_cuda(e, "extend workspace allocation");
+  e = launch_fwd_tc(a, st);
+  const cudaError_t ef = cudaFreeAsync(a.workspace, st);
+  if (e != cudaSuccess) return fail_cuda(e, "attn_sink_fwd_extend launch");
+  if (ef != cudaSuccess) return fail_cuda(ef, "extend workspace release");
+  return ATTN_OK;
 }
 
 }  // extern "C"

@@ -129,10 +129,44 @@ struct Params {
   float *max_logit;                        // [B, Hq] (stride ml_sb), kMaxLogit only
   int64_t ml_sb;
   // kPrior only: the sequences' keys are rows cu_seqlens_k[b] ..
-  // cu_seqlens_k[b+1]-1 of [Tk, Hkv, D] tensors
+  // cu_seqlens_k[b+1]-1 of [Tk, Hkv, D] tensors; a query tile is `ppt` positions of
+  // `pack` query heads of one kv head (row r: position r / pack, head r % pack);
+  // its keys go to `nsplit` units, whose partial O (f32, normalised) and log2-sums
+  // lie in o_part [units][128][D] and lse_part [units][128] when nsplit > 1.
   const int *cu_seqlens_k;
-  int Tk;
+  int Tk, pack, ppt, nsplit;
+  float *o_part, *lse_part;
 };
+
+// A kPrior unit: query tile, head group, sequence and its share of the key tiles.
+struct PriorUnit {
+  int m0, h0, b, row0, len, krow0, klen, pm0, kt0, n_tiles;
+};
+template <int BN>
+__device__ __forceinline__ PriorUnit prior_unit(const Params &p, int u) {
+  PriorUnit t;
+  const int sp = u % p.nsplit, x = u / p.nsplit;
+  const int groups = p.Hq / p.pack, per_m = groups * p.B;
+  const int mt = p.num_m_tiles - 1 - x / per_m;
+  const int r = x - (x / per_m) * per_m;
+  t.h0 = (r % groups) * p.pack;
+  t.b = r / groups;
+  t.m0 = mt * p.ppt;
+  // offsets clamped, so that a malformed table never moves an access outside
+  t.row0 = min(max(p.cu_seqlens[t.b], 0), p.T);
+  t.len = min(max(p.cu_seqlens[t.b + 1], t.row0), p.T) - t.row0;
+  t.krow0 = min(max(p.cu_seqlens_k[t.b], 0), p.Tk);
+  t.klen = min(max(p.cu_seqlens_k[t.b + 1], t.krow0), p.Tk) - t.krow0;
+  t.pm0 = t.m0 + t.klen - t.len;
+  const int last = min(t.klen - 1, t.pm0 + p.ppt - 1);   // (position of the tile's last row)
+  t.kt0 = max(0, t.pm0 - p.W + 1) / BN;
+  // a tile that sees no key still runs one, masked, for its zeros and LSE
+  const int n = t.m0 >= t.len ? 0 : last < 0 ? 1 : last / BN - t.kt0 + 1;
+  const int s0 = static_cast<int>(static_cast<int64_t>(n) * sp / p.nsplit);
+  t.n_tiles = static_cast<int>(static_cast<int64_t>(n) * (sp + 1) / p.nsplit) - s0;
+  t.kt0 += s0;
+  return t;
+}
 
 // Warp-uniform bounded wait: every lane learns the same outcome, so the
 // .sync.aligned tcgen05 instructions that follow stay convergent.
@@ -343,8 +377,10 @@ __device__ __forceinline__ void atomic_max_float(float *addr, float v) {
 }
 
 // kPrior (with kPacked): a sequence has keys of its own row range, usually more
-// than queries: its queries are the last positions (row i sits at position
-// i + klen - len, and sees nothing where that is negative).
+// than queries: its queries are the last positions (query i sits at position
+// i + klen - len, and sees nothing where that is negative).  Its query tiles hold
+// the grouped heads of a few positions instead of 128 positions of one head, so
+// that a chunk of few tokens fills them, and their keys may be split.
 // kMaxLogit: also the largest content logit scale*<q_i,k_j> over every row and
 // visible key of each (sequence, head), into Params::max_logit (atomic max).
 template <int D, int BN, int NH, bool kPacked, bool kMaxLogit, bool kPrior>
@@ -381,6 +417,7 @@ __global__ void __launch_bounds__(Cfg<D, BN, NH>::kThreads, Cfg<D, BN, NH>::kCta
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int HP = p.Hq / NH;                 // head groups (units per position and batch)
+  const int pack = kPrior ? p.pack : 1, ppt = kPrior ? p.ppt : kBM;   // heads and positions of a tile
   // Work units: (query tile, head group, batch), latest query tiles first (they
   // see the most keys under a causal window), head groups fastest so that the
   // CTAs running at the same time share K/V tiles in L2.  CTA c takes units
@@ -397,6 +434,20 @@ __global__ void __launch_bounds__(Cfg<D, BN, NH>::kThreads, Cfg<D, BN, NH>::kCta
   auto bc = [&](const Unit &t) { return packed ? 0 : t.b; };
   auto unit_at = [&](int u) {
     Unit t;
+    if constexpr (kPrior) {
+      const PriorUnit x = prior_unit<BN>(p, u);
+      t.m0 = x.m0;
+      t.h0 = x.h0;
+      t.b = x.b;
+      t.kt0 = x.kt0;
+      t.n_tiles = x.n_tiles;
+      t.len = x.len;
+      t.row0 = x.row0;
+      t.pm0 = x.pm0;
+      t.klen = x.klen;
+      t.krow0 = x.krow0;
+      return t;
+    }
     const int per_m = HP * p.B;
     const int mt = p.num_m_tiles - 1 - u / per_m;
     const int r = u - (u / per_m) * per_m;
@@ -412,20 +463,12 @@ __global__ void __launch_bounds__(Cfg<D, BN, NH>::kThreads, Cfg<D, BN, NH>::kCta
       t.row0 = 0;
       t.len = p.L;
     }
-    if constexpr (kPrior) {
-      t.krow0 = min(max(p.cu_seqlens_k[t.b], 0), p.Tk);
-      t.klen = min(max(p.cu_seqlens_k[t.b + 1], t.krow0), p.Tk) - t.krow0;
-      t.pm0 = t.m0 + t.klen - t.len;
-    } else {
-      t.krow0 = t.row0;
-      t.klen = t.len;
-      t.pm0 = t.m0;
-    }
-    const int row_last = min(t.klen - 1, t.pm0 + kBM - 1);   // (position of the tile's last row)
-    t.kt0 = max(0, t.pm0 - p.W + 1) / BN;
+    t.krow0 = t.row0;
+    t.klen = t.len;
+    t.pm0 = t.m0;
+    const int row_last = min(t.len - 1, t.m0 + kBM - 1);
+    t.kt0 = max(0, t.m0 - p.W + 1) / BN;
     t.n_tiles = t.m0 < t.len ? row_last / BN - t.kt0 + 1 : 0;
-    // a tile that sees no key still runs one, masked, for its zeros and LSE
-    if (kPrior && t.m0 < t.len && row_last < 0) t.n_tiles = 1;
     return t;
   };
 
@@ -502,7 +545,9 @@ __global__ void __launch_bounds__(Cfg<D, BN, NH>::kThreads, Cfg<D, BN, NH>::kCta
           ok = false;
           break;
         }
-        mbar_arrive_expect_tx(&q_full[qb], C::kQBufBytes);
+        // (kPrior: the box has ppt * pack rows; the tile's last rows keep old
+        // bytes, which only their own unused outputs see)
+        mbar_arrive_expect_tx(&q_full[qb], kPrior ? ppt * pack * D * 2 : C::kQBufBytes);
         for (int w = 0; w < NH; ++w)
           for (int c = 0; c < C::kChunks; ++c)
             tma_load_4d(sQ + qb * C::kQBufBytes + w * C::kQTileBytes + c * kBM * 128, &tmQ,
@@ -660,6 +705,10 @@ __global__ void __launch_bounds__(Cfg<D, BN, NH>::kThreads, Cfg<D, BN, NH>::kCta
     const int w = warp >> 2;                         // head slot of this warpgroup
     const int r = threadIdx.x & 127;                 // tile row == TMEM lane
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    // position and head of the row within the tile (kPrior: rows behind the last
+    // whole position repeat the first one and are not stored)
+    const bool r_used = !kPrior || r < ppt * pack;
+    const int r_pos = kPrior ? (r_used ? r / pack : 0) : r, r_head = kPrior ? (r_used ? r % pack : 0) : 0;
     const uint32_t o_col = C::kOCol(w);
     const float sl2 = p.scale_log2;
     bool ok = true;
@@ -671,9 +720,9 @@ __global__ void __launch_bounds__(Cfg<D, BN, NH>::kThreads, Cfg<D, BN, NH>::kCta
       if (packed && t.n_tiles <= 0) continue;
       ++ul;
       const int qb = ul & 1;
-      const int h = t.h0 + w;
-      const int i = t.m0 + r;                        // query row of the sequence
-      const int pi = t.pm0 + r;                      // and its position
+      const int h = t.h0 + w + r_head;
+      const int i = t.m0 + r_pos;                    // query row of the sequence
+      const int pi = t.pm0 + r_pos;                  // and its position
       float m_run = -INFINITY;                       // running max, log2 units
       float row_max = -INFINITY;                     // exact row maximum, log2 units
       float l_run = 0.f;                             // running denominator
@@ -689,7 +738,7 @@ __global__ void __launch_bounds__(Cfg<D, BN, NH>::kThreads, Cfg<D, BN, NH>::kCta
         const int kbase = (t.kt0 + j) * BN;
         // Tile-uniform test: does any (row, key) of this tile fall outside the
         // causal window or past the end of the sequence?
-        const bool edge = (kbase + BN - 1 > t.pm0) || (kbase < t.pm0 + kBM - p.W) || (kbase + BN > t.klen);
+        const bool edge = (kbase + BN - 1 > t.pm0) || (kbase < t.pm0 + ppt - p.W) || (kbase + BN > t.klen);
         const int lo = pi - p.W + 1 - kbase;         // first visible column
         const int hi = min(pi, t.klen - 1) - kbase;  // last visible column
         // Per 32-column chunk, a warp-uniform class: every lane's visible
@@ -769,7 +818,34 @@ __global__ void __launch_bounds__(Cfg<D, BN, NH>::kThreads, Cfg<D, BN, NH>::kCta
       // sequence's end belong to the next sequence).  Once O^w is out of TMEM
       // the next unit's PV^w may overwrite it.
       uint8_t *stage = sQ + qb * C::kQBufBytes + w * C::kQTileBytes;
-      const bool direct = packed && t.m0 + kBM > t.len;
+      const bool direct = packed && t.m0 + ppt > t.len;
+      const bool stored = r_used && i < t.len;
+      if constexpr (kPrior) {
+        if (p.nsplit > 1) {
+          // a share of the keys: O normalised in f32 and its log2-sum, merged
+          // by the combine kernel, which adds the sink
+          const int64_t slot = static_cast<int64_t>(u) * kBM + r;
+          const float inv = l_run != 0.f ? 1.f / l_run : 0.f;
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(lane_base + o_col + c * 32, o);
+            tmem_wait_ld_dep(o);
+            if (stored) {
+              float4 *po = reinterpret_cast<float4 *>(p.o_part + slot * D + c * 32);
+#pragma unroll
+              for (int uu = 0; uu < 8; ++uu)
+                po[uu] = make_float4(__uint_as_float(o[4 * uu]) * inv, __uint_as_float(o[4 * uu + 1]) * inv,
+                                     __uint_as_float(o[4 * uu + 2]) * inv, __uint_as_float(o[4 * uu + 3]) * inv);
+            }
+          }
+          if (stored) p.lse_part[slot] = l_run != 0.f ? m_run + log2f(l_run) : -INFINITY;
+          tc_fence_before();
+          mbar_arrive(&o_drained[w]);
+          if (r == 0) pending_qb = qb;
+          continue;
+        }
+      }
       // the next 32-column chunk is read while this one is converted
       auto convert = [&](int c, const uint32_t (&o)[32]) {
         uint8_t *chunk = stage + (c >> 1) * (kBM * 128) + r * 128;
@@ -781,7 +857,7 @@ __global__ void __launch_bounds__(Cfg<D, BN, NH>::kThreads, Cfg<D, BN, NH>::kCta
           v.z = pack_bf16x2(__uint_as_float(o[8 * uu + 4]) * oscale, __uint_as_float(o[8 * uu + 5]) * oscale);
           v.w = pack_bf16x2(__uint_as_float(o[8 * uu + 6]) * oscale, __uint_as_float(o[8 * uu + 7]) * oscale);
           if (direct) {
-            if (i < t.len)
+            if (stored)
               *reinterpret_cast<uint4 *>(p.out + static_cast<int64_t>(t.row0 + i) * p.o_sr +
                                          static_cast<int64_t>(h) * p.o_sh + c * 32 + uu * 8) = v;
           } else {
@@ -809,12 +885,12 @@ __global__ void __launch_bounds__(Cfg<D, BN, NH>::kThreads, Cfg<D, BN, NH>::kCta
       if (r == 0) {
         if (!direct) {
           for (int c = 0; c < C::kChunks; ++c)
-            tma_store_4d(&tmO, stage + c * kBM * 128, c * 64, h, t.row0 + t.m0, bc(t));
+            tma_store_4d(&tmO, stage + c * kBM * 128, c * 64, t.h0 + w, t.row0 + t.m0, bc(t));
           tma_store_commit();
         }
         pending_qb = qb;                           // released at the next unit's first tile
       }
-      if (p.lse != nullptr && i < t.len)
+      if (p.lse != nullptr && stored)
         p.lse[(packed ? t.row0 : static_cast<int64_t>(t.b) * p.lse_sb) + static_cast<int64_t>(h) * p.lse_sh +
               i] = lse_val;
       if constexpr (kMaxLogit) {
@@ -834,6 +910,80 @@ __global__ void __launch_bounds__(Cfg<D, BN, NH>::kThreads, Cfg<D, BN, NH>::kCta
   }
 }
 
+// Merges the partials of a kPrior tile whose keys were split, and adds the sink:
+// one warp per row, one block per kCombineRows rows of a tile.
+constexpr int kCombineRows = 8;
+template <int D, int BN>
+__global__ void __launch_bounds__(kCombineRows * 32) prior_combine_kernel(const __grid_constant__ Params p) {
+  constexpr int kPer = D / 32;                     // channels per lane, consecutive
+  const int lane = threadIdx.x & 31, r = blockIdx.y * kCombineRows + (threadIdx.x >> 5);
+  const int u0 = blockIdx.x * p.nsplit;
+  const PriorUnit t = prior_unit<BN>(p, u0 + min(lane, p.nsplit - 1));   // (lane s: split s)
+  const int i = t.m0 + r / p.pack, h = t.h0 + r % p.pack;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (r >= p.ppt * p.pack || i >= t.len) return;
+  const float sink2 = p.sinks[h] * kLog2e;
+  const bool there = lane < p.nsplit && t.n_tiles > 0;
+  const float ls = there ? p.lse_part[static_cast<int64_t>(u0 + lane) * kBM + r] : -INFINITY;
+  float M = fmaxf(ls, sink2);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  const float Mu = M == -INFINITY ? 0.f : M;
+  const float wt = there ? ex2_approx(ls - Mu) : 0.f;
+  float den = wt;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) den += __shfl_xor_sync(0xffffffffu, den, off);
+  den += ex2_approx(sink2 - Mu);
+  const uint32_t have = __ballot_sync(0xffffffffu, there);
+  float acc[kPer];
+#pragma unroll
+  for (int c = 0; c < kPer; ++c) acc[c] = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < p.nsplit; ++s) {              // splits in order
+    if (!(have >> s & 1u)) continue;
+    const float ws = __shfl_sync(0xffffffffu, wt, s);
+    const float *po = p.o_part + (static_cast<int64_t>(u0 + s) * kBM + r) * D + lane * kPer;
+#pragma unroll
+    for (int c = 0; c < kPer; c += 2) {
+      const float2 v = *reinterpret_cast<const float2 *>(po + c);
+      acc[c] = fmaf(ws, v.x, acc[c]);
+      acc[c + 1] = fmaf(ws, v.y, acc[c + 1]);
+    }
+  }
+  const float inv = den != 0.f ? 1.f / den : 0.f;
+  uint32_t *out = reinterpret_cast<uint32_t *>(p.out + static_cast<int64_t>(t.row0 + i) * p.o_sr +
+                                               static_cast<int64_t>(h) * p.o_sh + lane * kPer);
+#pragma unroll
+  for (int c = 0; c < kPer; c += 2) out[c / 2] = pack_bf16x2(acc[c] * inv, acc[c + 1] * inv);
+  if (p.lse != nullptr && lane == 0)
+    p.lse[t.row0 + static_cast<int64_t>(h) * p.lse_sh + i] = den != 0.f ? (Mu + log2f(den)) * kLn2 : -INFINITY;
+}
+
+// Query heads of a group that share a kPrior tile: the most that divide the group
+// and leave at most an eighth of the 128 rows unused (all of them up to 16).
+int prior_pack(int group) {
+  for (int d = group < kBM ? group : kBM; d > 1; --d)
+    if (group % d == 0 && kBM / d * d >= kBM - kBM / 8) return d;
+  return 1;
+}
+
+// Splits of a kPrior tile's keys.  Tiles that fill the machine are not split.
+// Fewer are split until they do, while a share keeps kSplitTiles key tiles by the
+// lengths the host knows (twice the mean number of keys, the window).
+constexpr int kSplitTiles = 4;
+int prior_splits(const FwdArgs &a, int ctas_per_sm, int sms) {
+  const int pack = prior_pack(a.Hq / a.Hkv), ppt = kBM / pack;
+  const int64_t tiles = static_cast<int64_t>((a.L + ppt - 1) / ppt) * (a.Hq / pack) * a.B;
+  const int64_t slots = static_cast<int64_t>(sms) * ctas_per_sm;
+  int64_t keys = 2 * (static_cast<int64_t>(a.Tk) / a.B + 1);
+  if (keys > a.Tk) keys = a.Tk;
+  if (keys > static_cast<int64_t>(a.W) + ppt) keys = static_cast<int64_t>(a.W) + ppt;
+  int64_t n = slots / tiles, most = keys / (64 * kSplitTiles);
+  if (n > most) n = most;
+  if (n > 32) n = 32;
+  return n < 2 ? 1 : static_cast<int>(n);
+}
+
 template <int D, int BN, int NH, bool kPacked, bool kMaxLogit = false, bool kPrior = false>
 cudaError_t launch(const FwdArgs &a, cudaStream_t stream) {
   using C = Cfg<D, BN, NH>;
@@ -842,7 +992,17 @@ cudaError_t launch(const FwdArgs &a, cudaStream_t stream) {
   // packed sequences: one [T, H, D] slice; else the [B, L, H, D] batch
   const int64_t nb = a.cu_seqlens != nullptr ? 1 : a.B;
   const int64_t nrow = a.cu_seqlens != nullptr ? a.T : a.L;
-  if ((e = make_tma_bshd(&mq, a.q, nb, nrow, a.Hq, D, a.q_s, kBM)) != cudaSuccess) return e;
+  Params p;
+  p.pack = 1;
+  p.ppt = kBM;
+  p.nsplit = 1;
+  p.o_part = p.lse_part = nullptr;
+  if (kPrior) {
+    p.pack = prior_pack(a.Hq / a.Hkv);
+    p.ppt = kBM / p.pack;
+  }
+  const int rows = kPrior ? p.ppt : kBM;
+  if ((e = make_tma_bshd(&mq, a.q, nb, nrow, a.Hq, D, a.q_s, rows, 2, p.pack)) != cudaSuccess) return e;
   // (no key at all: K and V are maps over Q, every row of which is masked)
   const bool no_keys = kPrior && a.Tk == 0;
   const int64_t krow = kPrior && !no_keys ? a.Tk : nrow;
@@ -850,15 +1010,21 @@ cudaError_t launch(const FwdArgs &a, cudaStream_t stream) {
     return e;
   if ((e = make_tma_bshd(&mv, no_keys ? a.q : a.v, nb, krow, a.Hkv, D, no_keys ? a.q_s : a.v_s, BN)) != cudaSuccess)
     return e;
-  if ((e = make_tma_bshd(&mo, a.out, nb, nrow, a.Hq, D, a.o_s, kBM)) != cudaSuccess) return e;
-  Params p;
+  if ((e = make_tma_bshd(&mo, a.out, nb, nrow, a.Hq, D, a.o_s, rows, 2, p.pack)) != cudaSuccess) return e;
   p.L = a.L;
   p.Hq = a.Hq;
   p.W = a.W;
   p.group = a.Hq / a.Hkv;
-  p.num_m_tiles = (a.L + kBM - 1) / kBM;
+  p.num_m_tiles = (a.L + rows - 1) / rows;
   p.B = a.B;
-  p.num_units = p.num_m_tiles * (a.Hq / NH) * a.B;
+  p.num_units = p.num_m_tiles * (a.Hq / NH / p.pack) * a.B;
+  if (kPrior && a.workspace != nullptr) {
+    p.nsplit = prior_splits(a, C::kCtasPerSm, a.sms);
+    const int64_t n = static_cast<int64_t>(p.num_units) * p.nsplit * kBM;
+    p.num_units *= p.nsplit;
+    p.o_part = static_cast<float *>(a.workspace);
+    p.lse_part = p.o_part + n * D;
+  }
   p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
   p.sinks = a.sinks;
   p.lse = a.lse;
@@ -896,7 +1062,17 @@ cudaError_t launch(const FwdArgs &a, cudaStream_t stream) {
   const int slots = sms * C::kCtasPerSm;
   dim3 grid(p.num_units < slots ? p.num_units : slots);
   kern<<<grid, C::kThreads, C::kSmemBytes, stream>>>(mq, mk, mv, mo, p);
-  return cudaGetLastError();
+  if ((e = cudaGetLastError()) != cudaSuccess || p.nsplit == 1) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.num_units / p.nsplit), kBM / kCombineRows);
+  cfg.blockDim = dim3(kCombineRows * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, prior_combine_kernel<D, BN>, p);
 }
 
 }  // namespace
@@ -906,6 +1082,14 @@ cudaError_t launch_max_logit_init(float *ml, int64_t sb, int B, int Hq, cudaStre
   if (n <= 0) return cudaSuccess;
   max_logit_init_kernel<<<(n + 255) / 256, 256, 0, stream>>>(ml, sb, B, Hq);
   return cudaGetLastError();
+}
+
+size_t fwd_extend_workspace_bytes(const FwdArgs &a) {
+  const int n = prior_splits(a, a.D <= 128 ? 2 : 1, a.sms);
+  if (n == 1) return 0;
+  const int pack = prior_pack(a.Hq / a.Hkv), ppt = kBM / pack;
+  const int64_t units = static_cast<int64_t>((a.L + ppt - 1) / ppt) * (a.Hq / pack) * a.B * n;
+  return static_cast<size_t>(units) * kBM * (a.D + 1) * sizeof(float);
 }
 
 cudaError_t launch_fwd_tc(const FwdArgs &a, cudaStream_t stream) {

@@ -32,6 +32,8 @@ struct FwdArgs {
   // positions).  Null: keys and queries share cu_seqlens.
   const int *cu_seqlens_k = nullptr;
   int Tk = 0;
+  int sms = 0;                             // (with cu_seqlens_k) multiprocessors
+  void *workspace = nullptr;               // fwd_extend_workspace_bytes, or null if that is 0
   // Largest content logit per (batch, query head): [B, Hq] f32 (row stride
   // ml_sb), batched inputs only; null: not computed.
   float *max_logit = nullptr;
@@ -128,6 +130,8 @@ int decode_max_splits_per_seq(const DecodeArgs &a);
 int decode_tile_keys(const DecodeArgs &a);
 
 cudaError_t launch_fwd_tc(const FwdArgs &a, cudaStream_t stream);
+// Workspace of a forward with cu_seqlens_k: partials, where it splits the keys.
+size_t fwd_extend_workspace_bytes(const FwdArgs &a);
 // Sets every entry of a [B, Hq] max-logit output to -inf.
 cudaError_t launch_max_logit_init(float *ml, int64_t sb, int B, int Hq, cudaStream_t stream);
 cudaError_t launch_fwd_cudacore(const FwdArgs &a, cudaStream_t stream);
@@ -141,8 +145,10 @@ cudaError_t launch_decode(const DecodeArgs &a, void *workspace, cudaStream_t str
 // {128, 1, box_rows, 1}: 128 one-byte elements per 128-byte swizzled row.
 // elem_bytes = 4 describes an f32 tensor with whole rows per box
 // ({d0, 1, box_rows, 1}, d0 <= 256, no swizzle), for bulk reductions.
+// box_heads consecutive heads of every position per box, heads innermost.
 cudaError_t make_tma_bshd(void *map_out, const void *base, int64_t d3, int64_t d2, int64_t d1,
-                          int64_t d0, const int64_t strides_el[3], int box_rows, int elem_bytes = 2);
+                          int64_t d0, const int64_t strides_el[3], int box_rows, int elem_bytes = 2,
+                          int box_heads = 1);
 // TMA descriptor of a bf16 page pool [npages, page, H, D] (element strides of
 // the first three dimensions in strides_el; the last one contiguous) as 5-D
 // (64 channels, position in page, 64-channel chunk, head, page) with 128-byte
