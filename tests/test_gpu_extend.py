@@ -117,7 +117,7 @@ def test_extend_without_earlier_keys_is_the_packed_forward(G):
 
 
 def test_extend_workspace_failure_launches_nothing():
-    q, k, v, cu_q, cu_k, sinks = _case(54, [2], [3000], 1, 2, 64, tail=(0, 0))
+    q, k, v, cu_q, cu_k, sinks = _case(54, [2], [3000], 1, 2, 64, tail=(0, 0))     # (keys are split)
     out = torch.full(q.shape, 9.0, dtype=torch.bfloat16, device=DEV)
     args = (q.to(DEV), k.to(DEV), v.to(DEV), _i32(cu_q), _i32(cu_k), 2, torch.from_numpy(sinks).to(DEV), 1 << 30, 0.1, out)
     swl.attn_sink_fail_workspace_allocs(1)
