@@ -47,7 +47,7 @@ namespace {
 constexpr uint32_t kBarInit = 1;      // named barrier: every thread, once
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
-enum : int { kWhereFull = 401, kWhereEmpty = 402, kWhereMerge = 403 };
+enum : int { kWhereFull = 401, kWhereEmpty = 402, kWhereMerge = 403, kWhereAlign = 404 };
 
 // The numerator's P is f16, up to 2^15: kHeadroom keeps it as far from the
 // subnormals as the lazy reference (exponents up to kLazy above it) allows.
@@ -93,10 +93,17 @@ Workspace layout(const PagedFp8Args &a, int teams) {
   return w;
 }
 
+// Where no sequence can have more tiles than this (a short window or a short
+// table), nothing is cut: an item is a sequence's kv head, there is no plan and no
+// combine launch.  One sequence in a window of 513, 4 kv heads, D = 128 (three
+// tiles): 10.1 us, cut and combined 11.4; 64 of them 17.4 us against 22.7.
+constexpr int kWholeTiles = 4;
+
 struct Params {
   PagedFp8Args a;
   int G, teams, page_shift, box_rows, box_shift;
   int out8;                              // rows of out keep 8-byte alignment
+  int whole;                             // nothing is cut (kWholeTiles)
   float scale_log2;
   int2 *info;
   float *lse_part, *o_part;
@@ -155,7 +162,7 @@ struct Cfg {
   // two slots, so that a piece's is ready before the previous one ends
   static constexpr int kQSlot = (D / 16) * NT * 32 * 8 + NT * 8 * 4;
   static constexpr int kQBytes = (2 * kQSlot + 127) / 128 * 128;
-  static constexpr int kFixed = 1024 /* alignment */ + kQBytes + 3 * kCW * 8 * 4 + 1024;
+  static constexpr int kFixed = kQBytes + 3 * kCW * 8 * 4 + 1024;
   static constexpr int kStagesRaw = (232448 - kFixed) / (kStageBytes + kScaleBytes + 64);
   static constexpr int kStages = kStagesRaw > 8 ? 8 : kStagesRaw;
   static constexpr int kQOffset = kStages * kStageBytes;
@@ -164,7 +171,7 @@ struct Cfg {
   // stage infos and barriers; the consumers' meeting, merge and q barriers; the
   // merge unit, (m, M, L) per warp and head, abort flag
   static constexpr int kTail = kStages * (32 + 16) + 8 * 8 + 32 + 3 * kCW * 8 * 4 + 32;
-  static constexpr int kSmemBytes = kInfoOffset + kTail + 1024;
+  static constexpr int kSmemBytes = kInfoOffset + kTail;
   static_assert(kStages >= 3, "ring");
   static_assert(kSmemBytes <= 232448, "shared-memory budget");
   static_assert(kCW * 8 * D * 4 <= kStageBytes, "one merge pass fits a stage");
@@ -208,9 +215,13 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                            const __grid_constant__ Params p) {
   using C = Cfg<D, NT>;
   asm volatile("griddepcontrol.launch_dependents;");
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem =
-      reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  // (128-byte swizzled boxes need 1024-byte aligned addresses; aligning by hand
+  // would hide from the compiler that this is shared memory)
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (reinterpret_cast<uintptr_t>(smem) & 1023u) {
+    if (threadIdx.x == 0) report_launch_error(p.a.status, kWhereAlign);
+    return;
+  }
   StageInfo *info = reinterpret_cast<StageInfo *>(smem + C::kInfoOffset);
   uint64_t *full = reinterpret_cast<uint64_t *>(info + C::kStages);
   uint64_t *empty = full + C::kStages;
@@ -255,38 +266,6 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     if (lead) {
       tma_prefetch_desc(&tmK);
       tma_prefetch_desc(&tmV);
-    }
-    // ---- plan: every producer warp finds the CTA's share for itself (the
-    // consumers need none of it).  Lane l counts the tiles of a run of sequences;
-    // a scan over the warp gives every run's first tile and the total.
-    const int per = (a.B + 31) / 32;
-    const int run0 = min(a.B, lane * per), run1 = min(a.B, run0 + per);
-    long long mine = 0;
-#pragma unroll 4
-    for (int b = run0; b < run1; ++b) mine += range_of<C::kTK>(p, a.seqlens[b]).tiles;
-    long long incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    const long long total = __shfl_sync(0xffffffffu, incl, 31);
-    const int E = static_cast<int>(min(static_cast<long long>(p.teams), total));   // spans in use
-    const int items = E * a.Hkv;
-    if (blockIdx.x == 0 && lead) p.info[p.teams] = make_int2(E, 0);
-    // spans of q + 1 tiles, rem of them, then of q
-    const long long span = E > 0 ? div_ll(total, E) : 0;
-    const long long rem = E > 0 ? total - span * E : 0;
-    auto span_start = [&](int j) { return j * span + min(static_cast<long long>(j), rem); };
-    // the first sequence of this CTA's first span, and its first tile
-    int b_from = 0;
-    long long base_from = 0;
-    if (static_cast<int>(blockIdx.x) < items) {
-      const long long first_tile = span_start(blockIdx.x / a.Hkv);
-      const uint32_t owner = __ballot_sync(0xffffffffu, incl - mine <= first_tile && first_tile < incl);
-      const int src = __ffs(owner) - 1;
-      b_from = __shfl_sync(0xffffffffu, run0, src);
-      base_from = __shfl_sync(0xffffffffu, incl - mine, src);
     }
     named_barrier_sync(kBarInit, C::kThreads);      // the barriers are initialised
     const int kv = lane >> 4, c = pw * C::kShare + (lane & 15);
@@ -438,87 +417,139 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[qs]);
     };
-    // (b, base): a sequence and its first tile; items come in the spans' order,
-    // and the walk of one begins where its span does
-    for (int item = blockIdx.x; ok && item < items; item += gridDim.x) {
-      const int team = item / a.Hkv, hk = item - team * a.Hkv;
-      const long long t0 = span_start(team), t1 = span_start(team + 1);
-      int2 note = make_int2(-1, 0);    // the sequence that begins in this span and is cut by its end
-      long long last_tile = 0;         // and its last tile
-      int b = b_from;
-      long long base = base_from;
-      Range r = range_of<C::kTK>(p, a.seqlens[b]);
-      long long t = t0;
-      while (ok && t < t1) {
-        while (t >= base + r.tiles) {
-          base += r.tiles;
-          r = range_of<C::kTK>(p, a.seqlens[++b]);
+    // Tiles i0 .. i1-1 of sequence b (range r), kv head hk, as one piece.
+    auto issue_piece = [&](int b, int hk, const Range &r, int i0, int i1, int dest) {
+      const int *table = a.block_table + static_cast<int64_t>(b) * a.bt_s0;
+      auto page_of = [&](int i) -> int {   // pool page of this lane's 16 keys of tile i
+        const int key = r.start + i * C::kTK + c * 16;
+        if (!active || i >= i1 || key >= r.n) return -1;
+        const int pg = table[key >> p.page_shift];
+        return pg >= 0 && pg < a.npages ? pg : -1;
+      };
+      int pg_next = page_of(i0);
+      for (int i = i0; ok && i < i1; ++i) {
+        const int pg = pg_next;
+        pg_next = page_of(i + 1);          // (read a tile ahead: its latency overlaps the stage wait)
+        const int key0 = r.start + i * C::kTK;
+        const int nvalid = min(C::kTK, r.n - key0);
+        const int s = acquire();
+        if (!ok) break;
+        // only the boxes that hold a valid key are loaded; the rest of the
+        // stage keeps old bytes, which are masked
+        const int nbox = (nvalid + rows - 1) >> p.box_shift;
+        if (lead) {
+          StageInfo &si = info[s];
+          si.b = b;
+          si.hk = hk;
+          si.dest = dest;
+          si.nvalid = nvalid;
+          si.nskip = max(0, r.vis0 - key0);
+          si.flags = (i == i0 ? 1 : 0) | (i == i1 - 1 ? 2 : 0);
+          mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(nbox) * rows * D * 2);
         }
-        if (t == t0) {
-          b_from = b;
-          base_from = base;
+        __syncwarp();
+        uint8_t *stage = smem + s * C::kStageBytes + kv * C::kTileBytes;
+        const int key = key0 + c * 16;
+        const int at = key & (a.page - 1);
+        // An entry outside the pool reads as a page of zero rows: the box is
+        // out of range and filled with zeros (it still delivers its bytes).
+        if (issues && c * 16 < nbox * rows)
+          tma_load_5d(stage + c * 16 * D, kv ? &tmV : &tmK, &full[s], 0, at, 0, hk, pg);
+        if (active && c * 16 < nvalid)
+          copy16_async(smem + C::kScaleOffset + s * C::kScaleBytes + kv * C::kTK + c * 16,
+                       scales + (pg < 0 ? 0 : pg * sc_page + hk * sc_head + at), pg >= 0);
+        copy_async_arrive(&full[s]);
+        if (i == i0) {
+          if (pw == C::kPW - 1) prepare_q(b, hk);
+          ++pieces;
         }
-        const int i0 = static_cast<int>(t - base);                               // first tile of the piece
-        const int i1 = static_cast<int>(min(static_cast<long long>(r.tiles), t1 - base));
-        const bool whole = i0 == 0 && i1 == r.tiles;
-        const int dest = whole ? -1 : 2 * team + (i0 == 0 ? 1 : 0);
-        if (i0 == 0 && i1 < r.tiles) {
-          note.x = b;
-          last_tile = base + r.tiles - 1;
-        }
-        const int *table = a.block_table + static_cast<int64_t>(b) * a.bt_s0;
-        auto page_of = [&](int i) -> int {   // pool page of this lane's 16 keys of tile i
-          const int key = r.start + i * C::kTK + c * 16;
-          if (!active || i >= i1 || key >= r.n) return -1;
-          const int pg = table[key >> p.page_shift];
-          return pg >= 0 && pg < a.npages ? pg : -1;
-        };
-        int pg_next = page_of(i0);
-        for (int i = i0; ok && i < i1; ++i) {
-          const int pg = pg_next;
-          pg_next = page_of(i + 1);          // (read a tile ahead: its latency overlaps the stage wait)
-          const int key0 = r.start + i * C::kTK;
-          const int nvalid = min(C::kTK, r.n - key0);
-          const int s = acquire();
-          if (!ok) break;
-          // only the boxes that hold a valid key are loaded; the rest of the
-          // stage keeps old bytes, which are masked
-          const int nbox = (nvalid + rows - 1) >> p.box_shift;
-          if (lead) {
-            StageInfo &si = info[s];
-            si.b = b;
-            si.hk = hk;
-            si.dest = dest;
-            si.nvalid = nvalid;
-            si.nskip = max(0, r.vis0 - key0);
-            si.flags = (i == i0 ? 1 : 0) | (i == i1 - 1 ? 2 : 0);
-            mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(nbox) * rows * D * 2);
-          }
-          __syncwarp();
-          uint8_t *stage = smem + s * C::kStageBytes + kv * C::kTileBytes;
-          const int key = key0 + c * 16;
-          const int at = key & (a.page - 1);
-          // An entry outside the pool reads as a page of zero rows: the box is
-          // out of range and filled with zeros (it still delivers its bytes).
-          if (issues && c * 16 < nbox * rows)
-            tma_load_5d(stage + c * 16 * D, kv ? &tmV : &tmK, &full[s], 0, at, 0, hk, pg);
-          if (active && c * 16 < nvalid)
-            copy16_async(smem + C::kScaleOffset + s * C::kScaleBytes + kv * C::kTK + c * 16,
-                         scales + (pg < 0 ? 0 : pg * sc_page + hk * sc_head + at), pg >= 0);
-          copy_async_arrive(&full[s]);
-          if (i == i0) {
-            if (pw == C::kPW - 1) prepare_q(b, hk);
-            ++pieces;
-          }
-          poll_merge();
-        }
-        t = base + i1;
+        if (merged < (pieces - 1) * NT) poll_merge();   // (an earlier piece's units are still to come)
       }
-      if (hk == 0 && lead) {
-        const long long wide = rem * (span + 1);    // tiles of the longer spans
-        if (note.x >= 0)
-          note.y = static_cast<int>(last_tile < wide ? div_ll(last_tile, span + 1) : rem + div_ll(last_tile - wide, span));
-        p.info[team] = note;
+    };
+    if (p.whole) {
+      // short sequences: one item is a whole sequence's kv head, nothing is cut
+      const int total_items = a.B * a.Hkv;
+      int n = static_cast<int>(blockIdx.x) < total_items ? a.seqlens[blockIdx.x / a.Hkv] : 0;
+      for (int item = blockIdx.x; ok && item < total_items; item += gridDim.x) {
+        const int b = item / a.Hkv, hk = item - b * a.Hkv, next = item + gridDim.x;
+        const Range r = range_of<C::kTK>(p, n);
+        if (next < total_items) n = a.seqlens[next / a.Hkv];
+        if (r.tiles > 0) {
+          issue_piece(b, hk, r, 0, r.tiles, -1);
+        } else {
+          for (int e = pw * 32 + lane; e < p.G * D; e += C::kPW * 32)
+            a.out[b * a.o_s[0] + (hk * p.G + e / D) * a.o_s[1] + e % D] = __float2bfloat16_rn(0.f);
+        }
+      }
+    } else {
+      // ---- plan: every producer warp finds the CTA's share for itself (the
+      // consumers need none of it).  Lane l counts the tiles of a run of sequences;
+      // a scan over the warp gives every run's first tile and the total.
+      const int per = (a.B + 31) / 32;
+      const int run0 = min(a.B, lane * per), run1 = min(a.B, run0 + per);
+      long long mine = 0;
+#pragma unroll 4
+      for (int b = run0; b < run1; ++b) mine += range_of<C::kTK>(p, a.seqlens[b]).tiles;
+      long long incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      const long long total = __shfl_sync(0xffffffffu, incl, 31);
+      const int E = static_cast<int>(min(static_cast<long long>(p.teams), total));   // spans in use
+      const int items = E * a.Hkv;
+      if (blockIdx.x == 0 && lead) p.info[p.teams] = make_int2(E, 0);
+      // spans of q + 1 tiles, rem of them, then of q
+      const long long span = E > 0 ? div_ll(total, E) : 0;
+      const long long rem = E > 0 ? total - span * E : 0;
+      auto span_start = [&](int j) { return j * span + min(static_cast<long long>(j), rem); };
+      // the first sequence of this CTA's first span, and its first tile
+      int b_from = 0;
+      long long base_from = 0;
+      if (static_cast<int>(blockIdx.x) < items) {
+        const long long first_tile = span_start(blockIdx.x / a.Hkv);
+        const uint32_t owner = __ballot_sync(0xffffffffu, incl - mine <= first_tile && first_tile < incl);
+        const int src = __ffs(owner) - 1;
+        b_from = __shfl_sync(0xffffffffu, run0, src);
+        base_from = __shfl_sync(0xffffffffu, incl - mine, src);
+      }
+      // (b, base): a sequence and its first tile; items come in the spans' order,
+      // and the walk of one begins where its span does
+      for (int item = blockIdx.x; ok && item < items; item += gridDim.x) {
+        const int team = item / a.Hkv, hk = item - team * a.Hkv;
+        const long long t0 = span_start(team), t1 = span_start(team + 1);
+        int2 note = make_int2(-1, 0);    // the sequence that begins in this span and is cut by its end
+        long long last_tile = 0;         // and its last tile
+        int b = b_from;
+        long long base = base_from;
+        Range r = range_of<C::kTK>(p, a.seqlens[b]);
+        long long t = t0;
+        while (ok && t < t1) {
+          while (t >= base + r.tiles) {
+            base += r.tiles;
+            r = range_of<C::kTK>(p, a.seqlens[++b]);
+          }
+          if (t == t0) {
+            b_from = b;
+            base_from = base;
+          }
+          const int i0 = static_cast<int>(t - base);                               // first tile of the piece
+          const int i1 = static_cast<int>(min(static_cast<long long>(r.tiles), t1 - base));
+          const bool whole = i0 == 0 && i1 == r.tiles;
+          if (i0 == 0 && i1 < r.tiles) {
+            note.x = b;
+            last_tile = base + r.tiles - 1;
+          }
+          issue_piece(b, hk, r, i0, i1, whole ? -1 : 2 * team + (i0 == 0 ? 1 : 0));
+          t = base + i1;
+        }
+        if (hk == 0 && lead) {
+          const long long wide = rem * (span + 1);    // tiles of the longer spans
+          if (note.x >= 0)
+            note.y = static_cast<int>(last_tile < wide ? div_ll(last_tile, span + 1) : rem + div_ll(last_tile - wide, span));
+          p.info[team] = note;
+        }
       }
     }
     if (ok) {
@@ -568,7 +599,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     return row_off + kb * 16 * C::kInner + ((u ^ swz) << 4);
   };
   uint32_t qf[C::kQInSmem ? 1 : D / 16][NT][2];   // B fragments of q^T per k-step and head tile
-  const uint2 *qsm = nullptr;                     // or where they are (this lane's)
+  int q_off = 0;                                  // where they are in shared memory
   float o[D / 16][NT][4];                         // O^T accumulators: [d tile][head tile][fragment]
   float sl[NT][2];                                // softmax scale of this lane's heads (with q's power of two)
   float n_ref[NT][2];                             // numerator reference - headroom (one per head, same in every lane)
@@ -586,9 +617,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       ++piece;
       const int qs = piece & 1;
       if (!warp_wait(&q_full[qs], static_cast<uint32_t>(piece >> 1) & 1u, ctx, kWhereFull)) break;
-      const uint8_t *slot_q = smem + C::kQOffset + qs * C::kQSlot;
-      qsm = reinterpret_cast<const uint2 *>(slot_q) + lane;
-      const float *qscale = reinterpret_cast<const float *>(slot_q + (D / 16) * NT * 32 * 8);
+      q_off = C::kQOffset + qs * C::kQSlot;
+      const uint2 *qsm = reinterpret_cast<const uint2 *>(smem + q_off) + lane;
+      const float *qscale = reinterpret_cast<const float *>(smem + q_off + (D / 16) * NT * 32 * 8);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         sl[nt][0] = qscale[nt * 8 + 2 * tig];
@@ -651,6 +682,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           for (int nt = 0; nt < NT; ++nt) {
             uint2 qa, qb;
             if constexpr (C::kQInSmem) {
+              const uint2 *qsm = reinterpret_cast<const uint2 *>(smem + q_off) + lane;
               qa = qsm[(kk * NT + nt) * 32];
               qb = qsm[((kk + 1) * NT + nt) * 32];
             } else {
@@ -956,7 +988,7 @@ __global__ void __launch_bounds__(128) paged_fp8_combine_kernel(const __grid_con
 }
 
 template <int D, int NT>
-cudaError_t launch(const Params &p, int sms, cudaStream_t stream) {
+cudaError_t launch(Params p, int sms, cudaStream_t stream) {
   using C = Cfg<D, NT>;
   const PagedFp8Args &a = p.a;
   alignas(64) CUtensorMap mk, mv;
@@ -966,9 +998,13 @@ cudaError_t launch(const Params &p, int sms, cudaStream_t stream) {
   auto split = paged_fp8_split_kernel<D, NT>;
   if ((e = cudaFuncSetAttribute(split, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes)) != cudaSuccess)
     return e;
-  const int64_t items = static_cast<int64_t>(p.teams) * a.Hkv;
+  const int64_t keys = (a.W < static_cast<int64_t>(a.max_pages) * a.page ? a.W : static_cast<int64_t>(a.max_pages) * a.page) +
+                       p.box_rows - 1;
+  const int64_t heads = static_cast<int64_t>(a.B) * a.Hkv;
+  p.whole = keys <= kWholeTiles * C::kTK && heads <= (1 << 30);
+  const int64_t items = p.whole ? heads : static_cast<int64_t>(p.teams) * a.Hkv;
   split<<<static_cast<unsigned>(items < sms ? items : sms), C::kThreads, C::kSmemBytes, stream>>>(mk, mv, p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if ((e = cudaGetLastError()) != cudaSuccess || p.whole) return e;
   const int64_t warps = static_cast<int64_t>(p.teams) * a.Hq + (a.B + 31) / 32;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((warps + 3) / 4));
