@@ -432,10 +432,11 @@ int attn_sink_cache_read_fp8(const attn_tensor *kpages, const attn_tensor *vpage
  *
  * Two launches on `stream`, no host synchronisation: the split kernel divides
  * the visible keys of the whole batch evenly over the SMs and finishes every
- * sequence that was not cut; a combine kernel merges the cut ones.  The result
+ * sequence that was not cut; a combine kernel merges the cut ones.  (One launch
+ * where min(window, MP * P) is so small that no sequence is cut.)  The result
  * does not depend on what else runs (no atomics).  Workspace, from the
- * library's stream-ordered pool: at most about 2 * (SMs / Hkv + 1) * Hq *
- * (D + 1) * 4 bytes, whatever the lengths.
+ * library's stream-ordered pool: at most 8 * max(SMs / Hkv, 1) * Hq * (D + 1) * 4
+ * bytes and a few KB, whatever the lengths.
  */
 int attn_sink_decode_paged_fp8(const attn_tensor *q, const attn_tensor *kpages, const attn_tensor *vpages,
                                const attn_tensor *kscales, const attn_tensor *vscales,

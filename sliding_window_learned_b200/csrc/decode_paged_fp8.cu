@@ -23,16 +23,32 @@
 //   combine  merges the spans of each cut sequence, in order, and adds the sink
 //            once; writes zeros for empty sequences.  Launched with programmatic
 //            dependence: its blocks are resident before the split ends.
-// At most two partials exist per span, whatever the lengths.
+// At most two partials exist per span, whatever the lengths.  Where all sequences
+// are short, items are whole sequences and the split is the only launch.
 //
-// Inside the split: producer warps stream tiles of 16 keys per consumer warp
-// into a ring of stages; each lane looks after 16 keys' page, the boxes go by
-// TMA (min(page, 64) positions x all D channels of a head) and the 16 scale bytes by
-// a 16-byte asynchronous copy, all counted on the stage's barrier.  A consumer
-// warp owns 16 keys of the tile: e4m3 is converted to f16 in registers (exact)
-// and both products run on warp-level f16 MMAs (heads are the N = 8 dimension),
-// q in f16 under a power-of-two scale per head.  The work is bound by HBM: D + 1
-// bytes per key, kv head and K or V.
+// Inside the split, twelve (D = 256: eight) consumer warps and four producer warps:
+//   consumers  a warp owns 16 (D = 64: 32) keys of every tile.  e4m3 is converted
+//              to f16 in registers (exact) and both products run on warp-level f16
+//              MMAs: S^T = K q^T and O^T += V^T P^T, heads the N = 8 dimension, q
+//              in f16 under a power-of-two scale per head.
+//   producers  find the CTA's share; stream the tiles into a ring of stages (a lane
+//              looks after 16 keys' page: boxes of min(page, 64) positions x all D
+//              channels of a head by TMA, the 16 scale bytes by a 16-byte
+//              asynchronous copy, all counted on the stage's barrier); one of
+//              them prepares each piece's q; and all four merge the consumers'
+//              states at the end of a piece while the consumers go on.
+//
+// Bound by HBM at long contexts: D + 1 bytes per key, kv head and K or V.  64
+// sequences of 4 K..131 K keys, Hq32 Hkv4 D128, 256-position pages: 643 us, 7.2
+// TB/s (1.10 of the measured copy rate, which reads and writes); 8 of them 110 us,
+// 6.1 TB/s, where the start (2.5 us to the first copies, then every CTA's first
+// stages at once) and the end show.  With 16 heads a group the consumers' chain of
+// dependent instructions bounds it: 5.3 TB/s.  Tried and dropped: K's codes straight
+// into e4m3 MMAs with q as two e4m3 terms (a quarter fewer instructions, but those
+// MMAs' latency is longer: 643 -> 720 us, 16 heads 503 -> 667); the consumers as
+// two groups that take tiles in turn with two key blocks a warp (110 -> 113 us, D =
+// 64 204 -> 304); one producer warp (its lanes' TMA copies are issued one after
+// another: pages of 16 positions 119 us against 74).
 #include <math.h>
 
 #include <type_traits>
