@@ -368,7 +368,7 @@ int attn_sink_decode_noalloc(const attn_tensor *q, const attn_tensor *kcache,
  *                     sequence, clamped to [0, MP * P].
  *
  * The same tensors go to each call, so that append then decode needs no other
- * bookkeeping than the lengths.  B <= 2^20, MP * P <= 2^30, Hkv <= 65535.
+ * bookkeeping than the lengths.  B <= 2^20, MP * P <= 2^30, Hkv <= 16384.
  */
 
 /*

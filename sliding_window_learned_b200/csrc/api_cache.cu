@@ -46,7 +46,7 @@ int check_pools(const attn_tensor *kpages, const attn_tensor *vpages, const attn
   if (block_table->shape[0] != seqlens->shape[0]) return fail(ATTN_EINVAL, "block_table and seqlens must have B rows");
   if (seqlens->shape[0] > 1 && seqlens->stride[0] != 1) return fail(ATTN_EINVAL, "seqlens must be contiguous");
   if (seqlens->shape[0] > (1 << 20) || o->NB > (1LL << 31) - 1 || o->MP > (1LL << 30) || o->MP * o->P > (1LL << 30) ||
-      o->Hkv > 65535)
+      o->Hkv > 16384)
     return fail(ATTN_EUNSUPPORTED, "B, Hkv, the pool or pages per sequence * page size too large");
   o->shift = 0;
   while ((1LL << o->shift) < o->P) ++o->shift;

@@ -26,7 +26,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 // Blocks of the one wave, per SM.  Measured at 8 x 16 K rows, 8 kv heads, D = 128
-// (4 / 3 / 2): append 122 / 130 / 152 us, read 146 / 143 / 131 us: the read's
+// (4 / 3 / 2): append 122 / 127 / 152 us, read 146 / 143 / 126 us: the read's
 // writes, two thirds of its bytes, do better from fewer places at a time.  A read
 // of few iterations is bound by latency instead and takes four (47 K rows of 2
 // heads, D = 64: 9.5 us, 10.9 with two).
@@ -46,13 +46,13 @@ struct Cfg {
 };
 
 struct Place {
-  int page;                            // pool page; -1: no place in the cache, -2: a row of no sequence
-  int at;                              // position within the page
+  int page;                            // pool page as the table has it; outside the pool: no place in the cache
+  int at;                              // position within the page; -1: a row of no sequence
 };
 
 // Where packed row r belongs: the last rows of each sequence, in order.
 __device__ __forceinline__ Place find_place(const CacheArgs &a, const int *cu, const int *seqlens, int64_t r) {
-  Place pl{-2, 0};
+  Place pl{-1, -1};
   if (r >= a.T) return pl;
   int lo = 0, hi = a.B;                // last b in [0, B) with cu[b] <= r
   while (hi - lo > 1) {
@@ -64,7 +64,7 @@ __device__ __forceinline__ Place find_place(const CacheArgs &a, const int *cu, c
   const int64_t cap = static_cast<int64_t>(a.max_pages) << a.page_shift;
   const int64_t n = min(max(static_cast<int64_t>(seqlens[lo]), static_cast<int64_t>(0)), cap);
   const int64_t pos = n - (end - r);
-  pl.page = -1;
+  pl.at = 0;
   if (pos < 0) return pl;
   pl.page = a.block_table[lo * a.bt_s0 + (pos >> a.page_shift)];
   pl.at = static_cast<int>(pos & ((1 << a.page_shift) - 1));
@@ -125,28 +125,31 @@ struct Vec {
   int row, head;
 };
 __device__ __forceinline__ Vec vec_of(const CacheArgs &a, const Walk &w, int i) {
+  // (head + i) / Hkv by a multiplication: head + i < Hkv + 32 and Hkv <= 16384, so
+  // the product's error stays below one part in Hkv
   Vec x;
-  x.row = static_cast<int>(static_cast<unsigned>(w.head + i) / static_cast<unsigned>(a.Hkv));
+  x.row = a.Hkv == 1 ? i : static_cast<int>(__umulhi(static_cast<unsigned>(w.head + i), a.hkv_inv));
   x.head = w.head + i - x.row * a.Hkv;
   return x;
 }
 
-// The place of the iteration's row `row`, from the lane that looked it up.
+// The place of the iteration's row `row`, from the lane that looked it up; page < 0
+// where there is none.
 __device__ __forceinline__ Place place_of(const CacheArgs &a, const Place &p, int row) {
   Place x;
   x.page = __shfl_sync(0xffffffffu, p.page, row);
   x.at = __shfl_sync(0xffffffffu, p.at, row);
   if (x.page >= a.npages) x.page = -1;
-  if (x.page < -2) x.page = -1;
   return x;
 }
 
-// Largest magnitude (bf16 bits without the sign) of 8 packed bf16.
-__device__ __forceinline__ uint32_t max_bits(const uint4 &x) {
-  const uint32_t m = 0x7FFF7FFFu;
-  const uint32_t t = __vmaxu2(__vmaxu2(x.x & m, x.y & m), __vmaxu2(x.z & m, x.w & m));
-  return max(t & 0xFFFFu, t >> 16);
+// Packed maximum of two bf16 pairs' magnitudes (a NaN in either half stays one).
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("{.reg .b32 x, y; abs.bf16x2 x, %1; abs.bf16x2 y, %2; max.NaN.bf16x2 %0, x, y;}" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
+__device__ __forceinline__ uint32_t max_abs8(const uint4 &x) { return max_abs2(max_abs2(x.x, x.y), max_abs2(x.z, x.w)); }
 
 // The magnitudes of a pair with those of its non-finite halves zeroed.
 __device__ __forceinline__ uint32_t finite_only(uint32_t x) {
@@ -184,16 +187,18 @@ __device__ __forceinline__ uint4 nan8(const uint4 &x) {
 // and the row's scale byte.  Every lane of the warp takes part.
 template <int kLanes>
 __device__ __forceinline__ void quantise(Half2 x, uint2 *lo, uint2 *hi, int *byte) {
-  uint32_t m = max(max_bits(x.lo), max_bits(x.hi));
+  // (bf16 bits without the sign; NaN 0x7FFF)
+  auto row_max = [](uint32_t m) {
 #pragma unroll
-  for (int o = 1; o < kLanes; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int o = 1; o < kLanes; o <<= 1) m = max_abs2(m, __shfl_xor_sync(0xffffffffu, m, o));
+    return max(m & 0xFFFFu, m >> 16);
+  };
+  uint32_t m = row_max(max_abs2(max_abs8(x.lo), max_abs8(x.hi)));
   // NaN or infinity in some row of the warp (rare): the maxima again, over the
   // finite magnitudes alone, and infinities become NaN (the conversion would
   // saturate them to a finite code)
   if (__any_sync(0xffffffffu, m >= 0x7F80u)) {
-    m = max(max_bits(finite8(x.lo)), max_bits(finite8(x.hi)));
-#pragma unroll
-    for (int o = 1; o < kLanes; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    m = row_max(max_abs2(max_abs8(finite8(x.lo)), max_abs8(finite8(x.hi))));
     x.lo = nan8(x.lo);
     x.hi = nan8(x.hi);
   }
@@ -207,7 +212,7 @@ __device__ __forceinline__ uint4 load16(const __nv_bfloat16 *p) { return *reinte
 __device__ __forceinline__ uint2 load8(const uint8_t *p) { return *reinterpret_cast<const uint2 *>(p); }
 
 template <int D, int kUnroll>
-__global__ void __launch_bounds__(kThreads) cache_append_kernel(const CacheArgs a) {
+__global__ void __launch_bounds__(kThreads, kAppendBlocks) cache_append_kernel(const CacheArgs a) {
   using C = Cfg<D, kUnroll>;
   __shared__ int stage[2 * kStageB + 1];
   Walk w = begin<C::kStep>(a, stage);
@@ -295,7 +300,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheArgs a)
       const Vec at = vec_of(a, w, i);
       const Place pl = place_of(a, place, i < w.left ? at.row : 0);
       // rows of no sequence stay as they are; a row without a place reads as zeros
-      row[u] = i < w.left && pl.page != -2 ? w.row + at.row : -1;
+      row[u] = i < w.left && pl.at >= 0 ? w.row + at.row : -1;
       head[u] = at.head;
       k0[u] = k1[u] = v0[u] = v1[u] = make_uint2(0, 0);
       kb[u] = vb[u] = 127;
@@ -337,6 +342,7 @@ cudaError_t launch_unrolled(CacheArgs a, bool append, int blocks_per_sm, int sms
   a.stride = blocks * kWarps * C::kStep;
   a.stride_rows = a.stride / a.Hkv;
   a.stride_heads = static_cast<int>(a.stride - a.stride_rows * a.Hkv);
+  a.hkv_inv = a.Hkv == 1 ? 0 : static_cast<uint32_t>(0x100000000ull / static_cast<uint64_t>(a.Hkv) + 1);
   kern<<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }

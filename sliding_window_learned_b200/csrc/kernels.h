@@ -102,6 +102,7 @@ struct CacheArgs {
   // (set by the launch) vectors between two iterations of a warp, as rows and heads
   int64_t stride = 0, stride_rows = 0;
   int stride_heads = 0;
+  uint32_t hkv_inv = 0;                    // 2^32 / Hkv, rounded up
 };
 cudaError_t launch_cache(const CacheArgs &a, bool append, int sms, cudaStream_t stream);
 

@@ -94,6 +94,7 @@ def test_append_and_read_are_exact(case):
     if table.size > 20:
         table[rng.integers(0, len(new)), rng.integers(0, MP)] = -1       # no page: dropped, reads zeros
         table[rng.integers(0, len(new)), rng.integers(0, MP)] = ref[0].shape[0]
+        table[rng.integers(0, len(new)), rng.integers(0, MP)] = -2
     k[0, 0, :4] = torch.tensor([INF, -INF, float("nan"), 0.0])
     v[-1] = 0.0
     pools = _pools(*ref)
@@ -152,6 +153,49 @@ def test_malformed_tables_stay_inside():
         swl.attn_sink_cache_read_fp8(*pools, _i32(table), _i32(bad_sl), _i32(bad_cu), *[o[1:-1] for o in out])
         for o in out:
             assert (o[0] == 3.0).all() and (o[-1] == 3.0).all()
+
+
+@pytest.mark.parametrize("bad", [-1, -2, -(1 << 31), 6, (1 << 31) - 1])
+def test_entries_outside_the_pool(bad):
+    """Every row of a page outside the pool is dropped by the append and read back as zeros."""
+    rng, table, sl, cu, k, v, ref = _append_case(5, [20, 9], [20, 9], 2, 64, 16, 2)
+    table[0, 0] = bad
+    pools = _pools(*ref)
+    args = (_i32(table), _i32(sl), _i32(cu))
+    swl.attn_sink_cache_append_fp8(k.to(DEV), v.to(DEV), *args, *pools)
+    cache8.append(inputs.bits(k), inputs.bits(v), table, sl, cu, *ref)
+    for got, want in zip(pools, ref):
+        np.testing.assert_array_equal(_u8(got), want)
+    out = [torch.full_like(x, 7.0, device=DEV) for x in (k, v)]
+    swl.attn_sink_cache_read_fp8(*pools, *args, *out)
+    for o, x in zip(out, cache8.read(*ref, table, sl, cu, k.shape[0])):
+        np.testing.assert_array_equal(o.double().cpu().numpy()[:29], x[:29])
+        assert (o[:16] == 0).all() and (o[29:] == 7.0).all()
+
+
+def test_a_pool_beyond_32_bits():
+    """Pages whose byte offsets pass 2^32 in the codes (4.6 GB a pool): written, read
+    back and attended to like the same rows in a small pool."""
+    rng = np.random.default_rng(6)
+    NB, P, Hkv, D, G, n = 70000, 64, 8, 128, 2, 200
+    e4, e8 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+    empty = lambda *s: torch.empty(*s, dtype=torch.uint8, device=DEV)  # noqa: E731
+    big = (empty(NB, P, Hkv, D).view(e4), empty(NB, P, Hkv, D).view(e4), empty(NB, Hkv, P).view(e8), empty(NB, Hkv, P).view(e8))
+    small = (empty(4, P, Hkv, D).view(e4), empty(4, P, Hkv, D).view(e4), empty(4, Hkv, P).view(e8), empty(4, Hkv, P).view(e8))
+    k, v = _rows(rng, n, Hkv, D).to(DEV), _rows(rng, n, Hkv, D).to(DEV)
+    q = _rows(rng, 1, Hkv * G, D, 1).to(DEV)
+    sl, cu, sinks = _i32([n]), _i32([0, n]), torch.zeros(Hkv * G, device=DEV)
+    outs = []
+    for pools, table in ((big, [[NB - 1, 65999, NB - 3, 69000]]), (small, [[3, 2, 0, 1]])):
+        t = _i32(table)
+        swl.attn_sink_cache_append_fp8(k, v, t, sl, cu, *pools)
+        ko, vo, out = torch.empty_like(k), torch.empty_like(v), torch.empty_like(q)
+        swl.attn_sink_cache_read_fp8(*pools, t, sl, cu, ko, vo)
+        swl.attn_sink_decode_paged_fp8(q, *pools, t, sl, sinks, 1 << 30, 0.1, out)
+        outs.append((ko, vo, out))
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+    assert swl.attn_sink_get_status() == 0
 
 
 # --------------------------------------------------------------------- decode
@@ -296,6 +340,40 @@ def test_decode_is_the_same_every_time():
     c = _decode_case(26, [3000, 100, 900], 47, 64, 2, 8, 128, 1 << 30)
     a, b = (_decode(*c, 1 << 30, 0.1) for _ in range(2))
     np.testing.assert_array_equal(a, b)
+
+
+def test_calls_on_two_streams_and_threads_at_once():
+    """Each with its own workspace: overlapping decodes give what they give alone."""
+    import threading
+    cases = [_decode_case(40 + i, [6000 + 500 * i, 300, 2000], 110, 64, 2, 8, 128, 1 << 30) for i in range(2)]
+    args = [(c[0].to(DEV), *_pools(*c[1:5]), _i32(c[5]), _i32(c[6]), torch.from_numpy(c[7]).to(DEV), 1 << 30, 0.1)
+            for c in cases]
+    want = []
+    for a in args:
+        want.append(torch.empty_like(a[0]))
+        swl.attn_sink_decode_paged_fp8(*a, want[-1])
+    torch.cuda.synchronize()
+    errors = []
+
+    def work(i):
+        try:
+            s = torch.cuda.Stream()
+            outs = [torch.empty_like(want[i]) for _ in range(40)]
+            s.wait_stream(torch.cuda.default_stream())
+            for o in outs:
+                swl.attn_sink_decode_paged_fp8(*args[i], o, stream=s)
+            s.synchronize()
+            assert all(torch.equal(o, want[i]) for o in outs)
+        except BaseException as e:
+            errors.append(e)
+
+    ts = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    assert not errors, errors
+    assert swl.attn_sink_get_status() == 0
 
 
 def test_decode_empty_table_and_batch():
