@@ -192,12 +192,17 @@ int attn_sink_decode_paged_fp8(const attn_tensor *q, const attn_tensor *kpages, 
   if ((rc = status_ptr(&a.status))) return rc;
   int sms;
   if ((rc = sm_count(&sms))) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const size_t bytes = paged_fp8_workspace_bytes(a, sms);
+  if (bytes == 0) {
+    const cudaError_t e = launch_decode_paged_fp8(a, nullptr, sms, st);
+    return e == cudaSuccess ? ATTN_OK : fail_cuda(e, "attn_sink_decode_paged_fp8 launch");
+  }
   cudaMemPool_t pool;
   if ((rc = workspace_pool(&pool))) return rc;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
   void *ws = nullptr;
   if (take_injected_alloc_failure()) return fail(ATTN_ENOMEM, "decode workspace allocation failed (injected)");
-  cudaError_t e = cudaMallocFromPoolAsync(&ws, paged_fp8_workspace_bytes(a, sms), pool, st);
+  cudaError_t e = cudaMallocFromPoolAsync(&ws, bytes, pool, st);
   if (e != cudaSuccess) return fail_cuda(e, "decode workspace allocation");
   e = launch_decode_paged_fp8(a, ws, sms, st);
   const cudaError_t ef = cudaFreeAsync(ws, st);

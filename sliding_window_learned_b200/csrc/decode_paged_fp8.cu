@@ -114,6 +114,12 @@ Workspace layout(const PagedFp8Args &a, int teams) {
 // combine launch.  One sequence in a window of 513, 4 kv heads, D = 128 (three
 // tiles): 10.1 us, cut and combined 11.4; 64 of them 17.4 us against 22.7.
 constexpr int kWholeTiles = 4;
+constexpr int tile_keys(int D) { return D == 64 ? 384 : D == 128 ? 192 : 128; }
+bool takes_whole(const PagedFp8Args &a) {
+  const int64_t cap = static_cast<int64_t>(a.max_pages) * a.page;
+  const int64_t keys = (a.W < cap ? a.W : cap) + (a.page < 64 ? a.page : 64) - 1;   // (from a box's start)
+  return keys <= kWholeTiles * tile_keys(a.D) && static_cast<int64_t>(a.B) * a.Hkv <= (1 << 30);
+}
 
 struct Params {
   PagedFp8Args a;
@@ -188,6 +194,7 @@ struct Cfg {
   // merge unit, (m, M, L) per warp and head, abort flag
   static constexpr int kTail = kStages * (32 + 16) + 8 * 8 + 32 + 3 * kCW * 8 * 4 + 32;
   static constexpr int kSmemBytes = kInfoOffset + kTail;
+  static_assert(kTK == tile_keys(D), "tile size");
   static_assert(kStages >= 3, "ring");
   static_assert(kSmemBytes <= 232448, "shared-memory budget");
   static_assert(kCW * 8 * D * 4 <= kStageBytes, "one merge pass fits a stage");
@@ -1004,7 +1011,7 @@ __global__ void __launch_bounds__(128) paged_fp8_combine_kernel(const __grid_con
 }
 
 template <int D, int NT>
-cudaError_t launch(Params p, int sms, cudaStream_t stream) {
+cudaError_t launch(const Params &p, int sms, cudaStream_t stream) {
   using C = Cfg<D, NT>;
   const PagedFp8Args &a = p.a;
   alignas(64) CUtensorMap mk, mv;
@@ -1014,11 +1021,7 @@ cudaError_t launch(Params p, int sms, cudaStream_t stream) {
   auto split = paged_fp8_split_kernel<D, NT>;
   if ((e = cudaFuncSetAttribute(split, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes)) != cudaSuccess)
     return e;
-  const int64_t keys = (a.W < static_cast<int64_t>(a.max_pages) * a.page ? a.W : static_cast<int64_t>(a.max_pages) * a.page) +
-                       p.box_rows - 1;
-  const int64_t heads = static_cast<int64_t>(a.B) * a.Hkv;
-  p.whole = keys <= kWholeTiles * C::kTK && heads <= (1 << 30);
-  const int64_t items = p.whole ? heads : static_cast<int64_t>(p.teams) * a.Hkv;
+  const int64_t items = p.whole ? static_cast<int64_t>(a.B) * a.Hkv : static_cast<int64_t>(p.teams) * a.Hkv;
   split<<<static_cast<unsigned>(items < sms ? items : sms), C::kThreads, C::kSmemBytes, stream>>>(mk, mv, p);
   if ((e = cudaGetLastError()) != cudaSuccess || p.whole) return e;
   const int64_t warps = static_cast<int64_t>(p.teams) * a.Hq + (a.B + 31) / 32;
@@ -1036,7 +1039,9 @@ cudaError_t launch(Params p, int sms, cudaStream_t stream) {
 
 }  // namespace
 
-size_t paged_fp8_workspace_bytes(const PagedFp8Args &a, int sms) { return layout(a, max_teams(a.Hkv, sms)).total; }
+size_t paged_fp8_workspace_bytes(const PagedFp8Args &a, int sms) {
+  return takes_whole(a) ? 0 : layout(a, max_teams(a.Hkv, sms)).total;
+}
 
 cudaError_t launch_decode_paged_fp8(const PagedFp8Args &a, void *workspace, int sms, cudaStream_t stream) {
   Params p;
@@ -1049,11 +1054,16 @@ cudaError_t launch_decode_paged_fp8(const PagedFp8Args &a, void *workspace, int 
   p.box_shift = p.page_shift < 6 ? p.page_shift : 6;
   p.out8 = (reinterpret_cast<uintptr_t>(a.out) | (a.o_s[0] * 2) | (a.o_s[1] * 2)) % 8 == 0;
   p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
-  const Workspace w = layout(a, p.teams);
-  uint8_t *ws = static_cast<uint8_t *>(workspace);
-  p.info = reinterpret_cast<int2 *>(ws + w.off_info);
-  p.lse_part = reinterpret_cast<float *>(ws + w.off_lse);
-  p.o_part = reinterpret_cast<float *>(ws + w.off_o);
+  p.whole = takes_whole(a);
+  p.info = nullptr;
+  p.lse_part = p.o_part = nullptr;
+  if (!p.whole) {
+    const Workspace w = layout(a, p.teams);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    p.info = reinterpret_cast<int2 *>(ws + w.off_info);
+    p.lse_part = reinterpret_cast<float *>(ws + w.off_lse);
+    p.o_part = reinterpret_cast<float *>(ws + w.off_o);
+  }
   switch (a.D) {
     case 64: return p.G <= 8 ? launch<64, 1>(p, sms, stream) : launch<64, 2>(p, sms, stream);
     case 128: return p.G <= 8 ? launch<128, 1>(p, sms, stream) : launch<128, 2>(p, sms, stream);

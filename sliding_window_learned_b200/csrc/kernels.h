@@ -118,6 +118,7 @@ struct PagedFp8Args {
   float scale;
   int *status;
 };
+// Workspace of one call; 0 where no sequence can be cut.
 size_t paged_fp8_workspace_bytes(const PagedFp8Args &a, int sms);
 cudaError_t launch_decode_paged_fp8(const PagedFp8Args &a, void *workspace, int sms, cudaStream_t stream);
 

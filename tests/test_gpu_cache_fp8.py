@@ -420,17 +420,21 @@ def test_decode_wait_runs_out_then_recovers():
 
 
 def test_decode_workspace_failure_launches_nothing():
-    c = _decode_case(29, [100], 2, 64, 1, 1, 64, 1 << 30)
+    c = _decode_case(29, [1900], 30, 64, 1, 1, 64, 1 << 30)
     out = torch.full((1, 1, 64), 5.0, dtype=torch.bfloat16, device=DEV)
+    args = (c[0].to(DEV), *_pools(*c[1:5]), _i32(c[5]), _i32(c[6]), torch.from_numpy(c[7]).to(DEV))
     swl.attn_sink_fail_workspace_allocs(1)
     try:
         with pytest.raises(swl.AttnSinkError) as e:
-            swl.attn_sink_decode_paged_fp8(c[0].to(DEV), *_pools(*c[1:5]), _i32(c[5]), _i32(c[6]),
-                                           torch.from_numpy(c[7]).to(DEV), 5, 0.1, out)
+            swl.attn_sink_decode_paged_fp8(*args, 1 << 30, 0.1, out)
         assert e.value.code == -4
+        assert (out == 5.0).all()
+        # sequences that are never cut need no workspace
+        swl.attn_sink_fail_workspace_allocs(1)
+        swl.attn_sink_decode_paged_fp8(*args, 5, 0.1, out)
+        assert (out != 5.0).any()
     finally:
         swl.attn_sink_fail_workspace_allocs(0)
-    assert (out == 5.0).all()
 
 
 def test_tensors_on_the_host_are_refused():
