@@ -180,19 +180,22 @@ struct Cfg {
   static constexpr int kTileBytes = kTK * D;
   static constexpr int kStageBytes = 2 * kTileBytes;        // K then V
   static constexpr int kScaleBytes = 2 * kTK;               // per stage: K then V
-  // a piece's q as B fragments [k-step][head tile][lane] and its heads' scales;
-  // two slots, so that a piece's is ready before the previous one ends
+  // a piece's q as B fragments [k-step][head tile][lane] and its heads' scales.
+  // One slot more than stages: when a piece's first tile has its stage, the piece
+  // kQSlots before has been released to its last tile, so a slot needs no barrier
+  // to say that it is free.
   static constexpr int kQSlot = (D / 16) * NT * 32 * 8 + NT * 8 * 4;
-  static constexpr int kQBytes = (2 * kQSlot + 127) / 128 * 128;
+  static constexpr int kQSlots = 5;
+  static constexpr int kQBytes = (kQSlots * kQSlot + 127) / 128 * 128;
   static constexpr int kFixed = kQBytes + 3 * kCW * 8 * 4 + 1024;
   static constexpr int kStagesRaw = (232448 - kFixed) / (kStageBytes + kScaleBytes + 64);
-  static constexpr int kStages = kStagesRaw > 8 ? 8 : kStagesRaw;
+  static constexpr int kStages = kStagesRaw > kQSlots - 1 ? kQSlots - 1 : kStagesRaw;
   static constexpr int kQOffset = kStages * kStageBytes;
   static constexpr int kScaleOffset = kQOffset + kQBytes;
   static constexpr int kInfoOffset = kScaleOffset + (kStages * kScaleBytes + 127) / 128 * 128;
   // stage infos and barriers; the consumers' meeting, merge and q barriers; the
   // merge unit, (m, M, L) per warp and head, abort flag
-  static constexpr int kTail = kStages * (32 + 16) + 8 * 8 + 32 + 3 * kCW * 8 * 4 + 32;
+  static constexpr int kTail = kStages * (32 + 16) + (3 + kQSlots) * 8 + 32 + 3 * kCW * 8 * 4 + 32;
   static constexpr int kSmemBytes = kInfoOffset + kTail;
   static_assert(kTK == tile_keys(D), "tile size");
   static_assert(kStages >= 3, "ring");
@@ -205,6 +208,19 @@ struct Cfg {
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const WaitCtx &ctx, int where) {
   const bool r = mbar_wait(bar, parity, ctx, where);
   return __all_sync(0xffffffffu, r);
+}
+
+// Whether the phase with the given parity is over, without waiting.
+__device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 __device__ __forceinline__ void mbar_arrive_n(uint64_t *bar, uint32_t n) {
@@ -251,9 +267,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
   uint64_t *meet = empty + C::kStages;       // the consumers are done with a piece's last stage
   uint64_t *merge_full = meet + 1;           // a merge unit is in shared memory
   uint64_t *merge_free = merge_full + 1;     // and has been read
-  uint64_t *q_full = merge_free + 1;         // [2] a piece's q is in its slot
-  uint64_t *q_free = q_full + 2;             // [2] and is no longer needed
-  MergeUnit *unit = reinterpret_cast<MergeUnit *>(q_free + 3);
+  uint64_t *q_full = merge_free + 1;         // [kQSlots] a piece's q is in its slot
+  MergeUnit *unit = reinterpret_cast<MergeUnit *>(q_full + C::kQSlots);
   float *merge_n = reinterpret_cast<float *>(unit + 1);             // numerator reference [kCW][8]
   float *merge_m = merge_n + C::kCW * 8;                            // softmax reference
   float *merge_l = merge_m + C::kCW * 8;                            // softmax sum
@@ -271,10 +286,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     mbar_init(meet, C::kCW);
     mbar_init(merge_full, C::kCW);
     mbar_init(merge_free, C::kPW);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&q_full[i], 1);
-      mbar_init(&q_free[i], C::kCW);
-    }
+    for (int i = 0; i < C::kQSlots; ++i) mbar_init(&q_full[i], 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -290,6 +302,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       tma_prefetch_desc(&tmK);
       tma_prefetch_desc(&tmV);
     }
+    // (short sequences: the first item's length, on its way while the CTA meets)
+    const int n_first = p.whole ? a.seqlens[min(static_cast<int>(blockIdx.x) / a.Hkv, a.B - 1)] : 0;
     named_barrier_sync(kBarInit, C::kThreads);      // the barriers are initialised
     const int kv = lane >> 4, c = pw * C::kShare + (lane & 15);
     const int rows = p.box_rows;
@@ -297,217 +311,21 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     const bool issues = active && (c * 16) % rows == 0;   // this lane's 16 keys start a box
     const uint8_t *scales = kv ? a.vscales : a.kscales;
     const int64_t sc_page = kv ? a.vs_s[0] : a.ks_s[0], sc_head = kv ? a.vs_s[1] : a.ks_s[1];
-    int slot = 0, pieces = 0, merged = 0;
-    bool ok = true;
-    // ---- merge units: the consumers leave a piece's partial states in its last
-    // stage and go on; every producer warp takes a share of the outputs ----
-    auto merge = [&]() {
-      const MergeUnit u = *unit;
-      const float *mbuf = reinterpret_cast<const float *>(smem + u.stage * C::kStageBytes);   // [warp][8 heads][D]
-      const int heads = min(p.G - u.nt * 8, 8);
-      for (int e = pw * 32 + lane; e < heads * (D / 4); e += C::kPW * 32) {
-        const int hl = e / (D / 4), d = (e - hl * (D / 4)) * 4;
-        const int hq = u.hk * p.G + u.nt * 8 + hl;
-        float M = kNoMax;
-#pragma unroll
-        for (int w = 0; w < C::kCW; ++w) M = fmaxf(M, merge_m[w * 8 + hl]);
-        // the sink joins here if no other span holds keys of this sequence
-        float den = 0.f;
-        if (u.dest < 0) {
-          const float sink2 = a.sinks[hq] * kLog2e;
-          M = fmaxf(M, sink2);
-          den = ex2_approx(sink2 - M);
-        }
-        float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < C::kCW; ++w) {
-          den += merge_l[w * 8 + hl] * ex2_approx(merge_m[w * 8 + hl] - M);
-          const float f = ex2_approx(merge_n[w * 8 + hl] - M);
-          const float4 v = *reinterpret_cast<const float4 *>(mbuf + (w * 8 + hl) * D + (d ^ (hl >> 1 << 3)));
-          num.x = fmaf(f, v.x, num.x);
-          num.y = fmaf(f, v.y, num.y);
-          num.z = fmaf(f, v.z, num.z);
-          num.w = fmaf(f, v.w, num.w);
-        }
-        const float inv = den != 0.f ? 1.f / den : 0.f;
-        num = make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
-        if (u.dest < 0) {
-          __nv_bfloat16 *po = a.out + u.b * a.o_s[0] + hq * a.o_s[1] + d;
-          if (p.out8) {
-            *reinterpret_cast<uint2 *>(po) = make_uint2(pack_bf16x2(num.x, num.y), pack_bf16x2(num.z, num.w));
-          } else {
-            po[0] = __float2bfloat16_rn(num.x);
-            po[1] = __float2bfloat16_rn(num.y);
-            po[2] = __float2bfloat16_rn(num.z);
-            po[3] = __float2bfloat16_rn(num.w);
-          }
-        } else {
-          const size_t row = static_cast<size_t>(u.dest) * a.Hq + hq;
-          *reinterpret_cast<float4 *>(p.o_part + row * D + d) = num;
-          if (d == 0) p.lse_part[row] = (M + log2f(den)) * kLn2;
-        }
-      }
-      // the generic reads are ordered before the next TMA write into the stage
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(merge_free);
-        if (u.last) mbar_arrive_n(&empty[u.stage], C::kCW / C::kPW);
-      }
-      ++merged;
-    };
-    // Merges the next unit if it is there; all lanes agree.
-    auto poll_merge = [&]() -> bool {
-      bool there = false;
-      if (lane == 0) there = mbar_try_wait(merge_full, static_cast<uint32_t>(merged) & 1u);
-      if (!__shfl_sync(0xffffffffu, there, 0)) return false;
-      __syncwarp();
-      merge();
-      return true;
-    };
-    // Bounded wait for `bar`, merging units meanwhile (the stage that is waited
-    // for may be one that a unit holds).
-    auto wait_or_merge = [&](uint64_t *bar, uint32_t parity, int where) -> bool {
-      uint64_t w0 = 0;
-      for (;;) {
-        int st = 0;                    // 1 there, 2 given up
-        if (lane == 0) {
-          if (ctx.limit >= kWaitSleepNs && mbar_try_wait(bar, parity)) st = 1;
-          else if (w0 == 0) w0 = globaltimer_ns();
-          else if (mbar_try_wait_sleep(bar, parity, ctx.limit < 1000 ? static_cast<uint32_t>(ctx.limit) : 1000u)) st = 1;
-          else if (*ctx.abort) st = 2;
-          else if (globaltimer_ns() - w0 > ctx.limit) {
-            report_timeout(ctx.status, where);
-            *ctx.abort = 1;
-            st = 2;
-          }
-        }
-        st = __shfl_sync(0xffffffffu, st, 0);
-        if (st == 1) return true;
-        if (st == 2) return false;
-        if (poll_merge()) w0 = 0;
-      }
-    };
-    auto acquire = [&]() -> int {
-      const int s = slot % C::kStages;
-      const uint32_t use = static_cast<uint32_t>(slot / C::kStages);
-      ok = ok && (slot < C::kStages || wait_or_merge(&empty[s], (use & 1u) ^ 1u, kWhereEmpty));
-      if (ok) ++slot;
-      return s;
-    };
-    // The last producer warp prepares a piece's q: f16 under a power of two per
-    // head that puts its largest magnitude in [2^13, 2^14) (exact for elements
-    // above max * 2^-27); k = 2t, 2t+1, 2t+8, 2t+9 of a k-step hold d = 4t .. 4t+3
-    // of its 16, the order K's bytes arrive in.
-    auto prepare_q = [&](int b, int hk) {
-      const int qs = pieces & 1;
-      if (pieces >= 2) ok = ok && wait_or_merge(&q_free[qs], static_cast<uint32_t>((pieces >> 1) - 1) & 1u, kWhereEmpty);
-      if (!ok) return;
-      uint2 *qsm = reinterpret_cast<uint2 *>(smem + C::kQOffset + qs * C::kQSlot) + lane;
-      float *qscale = reinterpret_cast<float *>(smem + C::kQOffset + qs * C::kQSlot + (D / 16) * NT * 32 * 8);
-      const int g8 = lane >> 2, tig = lane & 3;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        uint32_t x[D / 16][2];
-        const int hl = nt * 8 + g8;
-        const __nv_bfloat16 *qr = a.q + b * a.q_s[0] + (hk * p.G + hl) * a.q_s[1] + 4 * tig;
-        float mx = 0.f;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          x[kk][0] = x[kk][1] = 0u;
-          if (hl < p.G) {
-            x[kk][0] = *reinterpret_cast<const uint32_t *>(qr + kk * 16);
-            x[kk][1] = *reinterpret_cast<const uint32_t *>(qr + kk * 16 + 2);
-          }
-        }
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-#pragma unroll
-          for (int f = 0; f < 2; ++f)
-            mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(x[kk][f] << 16)), fabsf(__uint_as_float(x[kk][f] & 0xFFFF0000u))));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        int e = 0;
-        // (at most 2^126, so that the scale itself stays finite: a smaller q
-        // only lies lower in f16's range)
-        if (mx > 0.f && mx < INFINITY) e = min(13 - ilogbf(mx), 126);
-        const float sc = ldexpf(1.f, e);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          qsm[(kk * NT + nt) * 32] = make_uint2(f32x2_to_f16x2(x[kk][0], sc), f32x2_to_f16x2(x[kk][1], sc));
-        if (tig == 0) qscale[nt * 8 + g8] = ldexpf(p.scale_log2, -e);
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&q_full[qs]);
-    };
-    // Tiles i0 .. i1-1 of sequence b (range r), kv head hk, as one piece.
-    auto issue_piece = [&](int b, int hk, const Range &r, int i0, int i1, int dest) {
-      const int *table = a.block_table + static_cast<int64_t>(b) * a.bt_s0;
-      auto page_of = [&](int i) -> int {   // pool page of this lane's 16 keys of tile i
-        const int key = r.start + i * C::kTK + c * 16;
-        if (!active || i >= i1 || key >= r.n) return -1;
-        const int pg = table[key >> p.page_shift];
-        return pg >= 0 && pg < a.npages ? pg : -1;
-      };
-      int pg_next = page_of(i0);
-      for (int i = i0; ok && i < i1; ++i) {
-        const int pg = pg_next;
-        pg_next = page_of(i + 1);          // (read a tile ahead: its latency overlaps the stage wait)
-        const int key0 = r.start + i * C::kTK;
-        const int nvalid = min(C::kTK, r.n - key0);
-        const int s = acquire();
-        if (!ok) break;
-        // only the boxes that hold a valid key are loaded; the rest of the
-        // stage keeps old bytes, which are masked
-        const int nbox = (nvalid + rows - 1) >> p.box_shift;
-        if (lead) {
-          StageInfo &si = info[s];
-          si.b = b;
-          si.hk = hk;
-          si.dest = dest;
-          si.nvalid = nvalid;
-          si.nskip = max(0, r.vis0 - key0);
-          si.flags = (i == i0 ? 1 : 0) | (i == i1 - 1 ? 2 : 0);
-          mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(nbox) * rows * D * 2);
-        }
-        __syncwarp();
-        uint8_t *stage = smem + s * C::kStageBytes + kv * C::kTileBytes;
-        const int key = key0 + c * 16;
-        const int at = key & (a.page - 1);
-        // An entry outside the pool reads as a page of zero rows: the box is
-        // out of range and filled with zeros (it still delivers its bytes).
-        if (issues && c * 16 < nbox * rows)
-          tma_load_5d(stage + c * 16 * D, kv ? &tmV : &tmK, &full[s], 0, at, 0, hk, pg);
-        if (active && c * 16 < nvalid)
-          copy16_async(smem + C::kScaleOffset + s * C::kScaleBytes + kv * C::kTK + c * 16,
-                       scales + (pg < 0 ? 0 : pg * sc_page + hk * sc_head + at), pg >= 0);
-        copy_async_arrive(&full[s]);
-        if (i == i0) {
-          if (pw == C::kPW - 1) prepare_q(b, hk);
-          ++pieces;
-        }
-        if (merged < (pieces - 1) * NT) poll_merge();   // (an earlier piece's units are still to come)
-      }
-    };
+    const int step = gridDim.x;
+    int item = blockIdx.x, items;
+    // ---- plan: every producer warp finds the CTA's share for itself (the
+    // consumers need none of it).  Lane l counts the tiles of a run of sequences;
+    // a scan over the warp gives every run's first tile and the total.
+    int E = 0, n_next = n_first;
+    long long span = 0, rem = 0;         // spans of span + 1 tiles, rem of them, then of span
+    auto span_start = [&](int j) { return j * span + min(static_cast<long long>(j), rem); };
+    // the sequence that holds an item's first tile, and its own first tile: where
+    // the walk of the items of one span, and of the next, begins
+    int b_from = 0;
+    long long base_from = 0;
     if (p.whole) {
-      // short sequences: one item is a whole sequence's kv head, nothing is cut
-      const int total_items = a.B * a.Hkv;
-      int n = static_cast<int>(blockIdx.x) < total_items ? a.seqlens[blockIdx.x / a.Hkv] : 0;
-      for (int item = blockIdx.x; ok && item < total_items; item += gridDim.x) {
-        const int b = item / a.Hkv, hk = item - b * a.Hkv, next = item + gridDim.x;
-        const Range r = range_of<C::kTK>(p, n);
-        if (next < total_items) n = a.seqlens[next / a.Hkv];
-        if (r.tiles > 0) {
-          issue_piece(b, hk, r, 0, r.tiles, -1);
-        } else {
-          for (int e = pw * 32 + lane; e < p.G * D; e += C::kPW * 32)
-            a.out[b * a.o_s[0] + (hk * p.G + e / D) * a.o_s[1] + e % D] = __float2bfloat16_rn(0.f);
-        }
-      }
+      items = a.B * a.Hkv;
     } else {
-      // ---- plan: every producer warp finds the CTA's share for itself (the
-      // consumers need none of it).  Lane l counts the tiles of a run of sequences;
-      // a scan over the warp gives every run's first tile and the total.
       const int per = (a.B + 31) / 32;
       const int run0 = min(a.B, lane * per), run1 = min(a.B, run0 + per);
       long long mine = 0;
@@ -520,75 +338,297 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         if (lane >= o) incl += y;
       }
       const long long total = __shfl_sync(0xffffffffu, incl, 31);
-      const int E = static_cast<int>(min(static_cast<long long>(p.teams), total));   // spans in use
-      const int items = E * a.Hkv;
+      E = static_cast<int>(min(static_cast<long long>(p.teams), total));   // spans in use
+      items = E * a.Hkv;
       if (blockIdx.x == 0 && lead) p.info[p.teams] = make_int2(E, 0);
-      // spans of q + 1 tiles, rem of them, then of q
-      const long long span = E > 0 ? div_ll(total, E) : 0;
-      const long long rem = E > 0 ? total - span * E : 0;
-      auto span_start = [&](int j) { return j * span + min(static_cast<long long>(j), rem); };
-      // the first sequence of this CTA's first span, and its first tile
-      int b_from = 0;
-      long long base_from = 0;
-      if (static_cast<int>(blockIdx.x) < items) {
-        const long long first_tile = span_start(blockIdx.x / a.Hkv);
+      if (item < items) {
+        span = div_ll(total, E);
+        rem = total - span * E;
+        const long long first_tile = span_start(item / a.Hkv);
         const uint32_t owner = __ballot_sync(0xffffffffu, incl - mine <= first_tile && first_tile < incl);
         const int src = __ffs(owner) - 1;
         b_from = __shfl_sync(0xffffffffu, run0, src);
         base_from = __shfl_sync(0xffffffffu, incl - mine, src);
       }
-      // (b, base): a sequence and its first tile; items come in the spans' order,
-      // and the walk of one begins where its span does
-      for (int item = blockIdx.x; ok && item < items; item += gridDim.x) {
-        const int team = item / a.Hkv, hk = item - team * a.Hkv;
-        const long long t0 = span_start(team), t1 = span_start(team + 1);
-        int2 note = make_int2(-1, 0);    // the sequence that begins in this span and is cut by its end
-        long long last_tile = 0;         // and its last tile
-        int b = b_from;
-        long long base = base_from;
-        Range r = range_of<C::kTK>(p, a.seqlens[b]);
-        long long t = t0;
-        while (ok && t < t1) {
-          while (t >= base + r.tiles) {
-            base += r.tiles;
-            r = range_of<C::kTK>(p, a.seqlens[++b]);
+    }
+
+    // ---- the pieces, one after another: tiles i .. i1-1 of sequence b (range r),
+    // kv head hk, for the partial slot dest (-1: the sequence is finished here)
+    int b = 0, hk = 0, i = 0, i1 = 0, i_first = 0, dest = -1, team = 0;
+    long long t = 0, t1 = 0, base = 0;
+    int note = -1;                       // the sequence that begins in this span and is cut by its end
+    long long note_tile = 0;             // and its last tile
+    Range r{};
+    bool in_item = false;
+    auto next_piece = [&]() -> bool {
+      if (p.whole) {
+        for (; item < items; item += step) {
+          b = item / a.Hkv;
+          hk = item - b * a.Hkv;
+          r = range_of<C::kTK>(p, n_next);
+          if (item + step < items) n_next = a.seqlens[(item + step) / a.Hkv];
+          if (r.tiles > 0) {
+            i = i_first = 0;
+            i1 = r.tiles;
+            item += step;
+            return true;
           }
-          if (t == t0) {
-            b_from = b;
-            base_from = base;
-          }
-          const int i0 = static_cast<int>(t - base);                               // first tile of the piece
-          const int i1 = static_cast<int>(min(static_cast<long long>(r.tiles), t1 - base));
-          const bool whole = i0 == 0 && i1 == r.tiles;
-          if (i0 == 0 && i1 < r.tiles) {
-            note.x = b;
-            last_tile = base + r.tiles - 1;
-          }
-          issue_piece(b, hk, r, i0, i1, whole ? -1 : 2 * team + (i0 == 0 ? 1 : 0));
-          t = base + i1;
+          for (int e = pw * 32 + lane; e < p.G * D; e += C::kPW * 32)
+            a.out[b * a.o_s[0] + (hk * p.G + e / D) * a.o_s[1] + e % D] = __float2bfloat16_rn(0.f);
         }
+        return false;
+      }
+      if (in_item && t >= t1) {          // the item is issued
         if (hk == 0 && lead) {
           const long long wide = rem * (span + 1);    // tiles of the longer spans
-          if (note.x >= 0)
-            note.y = static_cast<int>(last_tile < wide ? div_ll(last_tile, span + 1) : rem + div_ll(last_tile - wide, span));
-          p.info[team] = note;
+          int2 out = make_int2(note, 0);
+          if (note >= 0)
+            out.y = static_cast<int>(note_tile < wide ? div_ll(note_tile, span + 1) : rem + div_ll(note_tile - wide, span));
+          p.info[team] = out;
+        }
+        in_item = false;
+        item += step;
+      }
+      if (!in_item) {
+        if (item >= items) return false;
+        team = item / a.Hkv;
+        hk = item - team * a.Hkv;
+        t = span_start(team);
+        t1 = span_start(team + 1);
+        b = b_from;
+        base = base_from;
+        r = range_of<C::kTK>(p, a.seqlens[b]);
+        note = -1;
+      }
+      while (t >= base + r.tiles) {
+        base += r.tiles;
+        r = range_of<C::kTK>(p, a.seqlens[++b]);
+      }
+      if (!in_item) {
+        b_from = b;
+        base_from = base;
+        in_item = true;
+      }
+      i = i_first = static_cast<int>(t - base);
+      i1 = static_cast<int>(min(static_cast<long long>(r.tiles), t1 - base));
+      if (i == 0 && i1 < r.tiles) {
+        note = b;
+        note_tile = base + r.tiles - 1;
+      }
+      dest = i == 0 && i1 == r.tiles ? -1 : 2 * team + (i == 0 ? 1 : 0);
+      t = base + i1;
+      return true;
+    };
+    auto page_of = [&](int tile) -> int {   // pool page of this lane's 16 keys of a tile
+      const int key = r.start + tile * C::kTK + c * 16;
+      if (!active || tile >= i1 || key >= r.n) return -1;
+      const int pg = a.block_table[static_cast<int64_t>(b) * a.bt_s0 + (key >> p.page_shift)];
+      return pg >= 0 && pg < a.npages ? pg : -1;
+    };
+    // The last producer warp prepares a piece's q: f16 under a power of two per
+    // head that puts its largest magnitude in [2^13, 2^14) (exact for elements
+    // above max * 2^-27); k = 2t, 2t+1, 2t+8, 2t+9 of a k-step hold d = 4t .. 4t+3
+    // of its 16, the order K's bytes arrive in.  Its loads leave before the piece's
+    // first tile is issued, the rest follows it.
+    uint32_t qx[NT][D / 16][2];
+    auto load_q = [&]() {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int hl = nt * 8 + (lane >> 2);
+        const __nv_bfloat16 *qr = a.q + b * a.q_s[0] + (hk * p.G + hl) * a.q_s[1] + 4 * (lane & 3);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          qx[nt][kk][0] = qx[nt][kk][1] = 0u;
+          if (hl < p.G) {
+            qx[nt][kk][0] = *reinterpret_cast<const uint32_t *>(qr + kk * 16);
+            qx[nt][kk][1] = *reinterpret_cast<const uint32_t *>(qr + kk * 16 + 2);
+          }
         }
       }
-    }
-    if (ok) {
-      const int s = acquire();
-      if (ok) {
+    };
+    auto prepare_q = [&](int qs) {
+      uint2 *qsm = reinterpret_cast<uint2 *>(smem + C::kQOffset + qs * C::kQSlot) + lane;
+      float *qscale = reinterpret_cast<float *>(smem + C::kQOffset + qs * C::kQSlot + (D / 16) * NT * 32 * 8);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float mx = 0.f;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+          for (int f = 0; f < 2; ++f)
+            mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(qx[nt][kk][f] << 16)), fabsf(__uint_as_float(qx[nt][kk][f] & 0xFFFF0000u))));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        // 13 - floor(log2 mx), from the exponent's bits; at most 126, so that the
+        // scale itself stays finite (a smaller q only lies lower in f16's range);
+        // 0 where the head holds an infinity
+        const int eb = static_cast<int>(__float_as_uint(mx) >> 23);
+        const int e = eb == 255 ? 0 : min(140 - eb, 126);
+        const float sc = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          qsm[(kk * NT + nt) * 32] = make_uint2(f32x2_to_f16x2(qx[nt][kk][0], sc), f32x2_to_f16x2(qx[nt][kk][1], sc));
+        if ((lane & 3) == 0)
+          qscale[nt * 8 + (lane >> 2)] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[qs]);
+    };
+
+    // ---- one loop: issue tiles, then the end mark, then wait for the last merges;
+    // before each, merge what the consumers have left meanwhile (one copy of that
+    // code: every copy is fetched cold where it first runs)
+    int slot = 0, pieces = 0, merged = 0, pg_next = -1, qs = 0;
+    enum { kTiles, kMark, kRest };
+    int job = kTiles;
+    bool ok = true;
+    for (;;) {
+      if (job == kTiles && i == i1) {
+        if (next_piece()) {
+          pg_next = page_of(i);
+          if (pw == C::kPW - 1) load_q();
+        } else {
+          job = kMark;
+        }
+      }
+      const int s = slot % C::kStages;
+      const uint32_t parity = (static_cast<uint32_t>(slot / C::kStages) & 1u) ^ 1u;
+      // Bounded wait for the stage (the last job: for every unit to be merged),
+      // merging units meanwhile: the stage may be one that a unit holds.
+      uint64_t w0 = 0;
+      for (;;) {
+        int st = 0;                      // 1 the stage is free, 2 given up, 3 a unit to merge
+        if (lane == 0) {
+          if (merged < pieces * NT && mbar_test_wait(merge_full, static_cast<uint32_t>(merged) & 1u)) st = 3;
+          else if (job == kRest) st = merged == pieces * NT ? 1 : 0;
+          else if (slot < C::kStages || mbar_test_wait(&empty[s], parity)) st = 1;
+          if (st == 0) {
+            if (w0 == 0) {
+              w0 = globaltimer_ns();
+            } else if (*ctx.abort) {
+              st = 2;
+            } else if (globaltimer_ns() - w0 > ctx.limit) {
+              report_timeout(ctx.status, job == kRest ? kWhereMerge : kWhereEmpty);
+              *ctx.abort = 1;
+              st = 2;
+            } else {
+              const uint32_t nap = ctx.limit < 500 ? static_cast<uint32_t>(ctx.limit) : 500u;
+              if (job == kRest) mbar_try_wait_sleep(merge_full, static_cast<uint32_t>(merged) & 1u, nap);
+              else if (mbar_try_wait_sleep(&empty[s], parity, nap)) st = 1;
+            }
+          }
+        }
+        st = __shfl_sync(0xffffffffu, st, 0);
+        __syncwarp();
+        if (st == 2) ok = false;
+        if (st == 1 || st == 2) break;
+        if (st == 3) {
+          const MergeUnit u = *unit;
+          const float *mbuf = reinterpret_cast<const float *>(smem + u.stage * C::kStageBytes);   // [warp][8 heads][D]
+          const int heads = min(p.G - u.nt * 8, 8);
+          for (int e = pw * 32 + lane; e < heads * (D / 4); e += C::kPW * 32) {
+            const int hl = e / (D / 4), d = (e - hl * (D / 4)) * 4;
+            const int hq = u.hk * p.G + u.nt * 8 + hl;
+            // (first, so that its latency overlaps the sums; the sink joins here if no
+            // other span holds keys of this sequence)
+            const float sink2 = u.dest < 0 ? a.sinks[hq] * kLog2e : -INFINITY;
+            float M = kNoMax;
+#pragma unroll
+            for (int w = 0; w < C::kCW; ++w) M = fmaxf(M, merge_m[w * 8 + hl]);
+            float den = 0.f;
+            float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < C::kCW; ++w) {
+              den += merge_l[w * 8 + hl] * ex2_approx(merge_m[w * 8 + hl] - M);
+              const float f = ex2_approx(merge_n[w * 8 + hl] - M);
+              const float4 v = *reinterpret_cast<const float4 *>(mbuf + (w * 8 + hl) * D + (d ^ (hl >> 1 << 3)));
+              num.x = fmaf(f, v.x, num.x);
+              num.y = fmaf(f, v.y, num.y);
+              num.z = fmaf(f, v.z, num.z);
+              num.w = fmaf(f, v.w, num.w);
+            }
+            // on the larger of the keys' and the sink's reference: no exponent is positive
+            const float M1 = fmaxf(M, sink2), back = ex2_approx(M - M1);
+            den = den * back + ex2_approx(sink2 - M1);
+            const float inv = den != 0.f ? back / den : 0.f;
+            num = make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
+            if (u.dest < 0) {
+              __nv_bfloat16 *po = a.out + u.b * a.o_s[0] + hq * a.o_s[1] + d;
+              if (p.out8) {
+                *reinterpret_cast<uint2 *>(po) = make_uint2(pack_bf16x2(num.x, num.y), pack_bf16x2(num.z, num.w));
+              } else {
+                po[0] = __float2bfloat16_rn(num.x);
+                po[1] = __float2bfloat16_rn(num.y);
+                po[2] = __float2bfloat16_rn(num.z);
+                po[3] = __float2bfloat16_rn(num.w);
+              }
+            } else {
+              const size_t row = static_cast<size_t>(u.dest) * a.Hq + hq;
+              *reinterpret_cast<float4 *>(p.o_part + row * D + d) = num;
+              if (d == 0) p.lse_part[row] = (M1 + log2f(den)) * kLn2;
+            }
+          }
+          // the generic reads are ordered before the next TMA write into the stage
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(merge_free);
+            if (u.last) mbar_arrive_n(&empty[u.stage], C::kCW / C::kPW);
+          }
+          ++merged;
+          w0 = 0;
+        }
+      }
+      if (!ok || job == kRest) break;
+      ++slot;
+      if (job == kMark) {
         if (lead) {
           info[s].flags = 4;
           mbar_arrive(&full[s]);
         }
         __syncwarp();
         copy_async_arrive(&full[s]);
+        job = kRest;
+        continue;
       }
+      // ---- tile i into stage s ----
+      const int pg = pg_next;
+      pg_next = page_of(i + 1);            // (read a tile ahead: its latency overlaps the next wait)
+      const int key0 = r.start + i * C::kTK;
+      const int nvalid = min(C::kTK, r.n - key0);
+      // only the boxes that hold a valid key are loaded; the rest of the
+      // stage keeps old bytes, which are masked
+      const int nbox = (nvalid + rows - 1) >> p.box_shift;
+      const bool first = i == i_first;
+      if (lead) {
+        StageInfo &si = info[s];
+        si.b = b;
+        si.hk = hk;
+        si.dest = dest;
+        si.nvalid = nvalid;
+        si.nskip = max(0, r.vis0 - key0);
+        si.flags = (first ? 1 : 0) | (i == i1 - 1 ? 2 : 0);
+        mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(nbox) * rows * D * 2);
+      }
+      __syncwarp();
+      uint8_t *stage = smem + s * C::kStageBytes + kv * C::kTileBytes;
+      const int key = key0 + c * 16;
+      const int at = key & (a.page - 1);
+      // An entry outside the pool reads as a page of zero rows: the box is
+      // out of range and filled with zeros (it still delivers its bytes).
+      if (issues && c * 16 < nbox * rows)
+        tma_load_5d(stage + c * 16 * D, kv ? &tmV : &tmK, &full[s], 0, at, 0, hk, pg);
+      if (active && c * 16 < nvalid)
+        copy16_async(smem + C::kScaleOffset + s * C::kScaleBytes + kv * C::kTK + c * 16,
+                     scales + (pg < 0 ? 0 : pg * sc_page + hk * sc_head + at), pg >= 0);
+      copy_async_arrive(&full[s]);
+      if (first) {
+        if (pw == C::kPW - 1) prepare_q(qs);
+        qs = qs + 1 == C::kQSlots ? 0 : qs + 1;
+        ++pieces;
+      }
+      ++i;
     }
-    // the units still to come (the last one's stage stays taken: its consumers
-    // are done with the ring)
-    while (ok && merged < pieces * NT) ok = wait_or_merge(merge_full, static_cast<uint32_t>(merged) & 1u, kWhereMerge) && (poll_merge(), true);
     // Every copy has landed before this warp leaves: the CTA's shared memory
     // outlives them, also when the consumers gave up early (each wait is bounded
     // by the fixed limit, whatever limit the other waits use).
@@ -638,8 +678,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     if (si.flags & 1) {
       // a piece begins: its queries
       ++piece;
-      const int qs = piece & 1;
-      if (!warp_wait(&q_full[qs], static_cast<uint32_t>(piece >> 1) & 1u, ctx, kWhereFull)) break;
+      const int qs = piece % C::kQSlots;
+      if (!warp_wait(&q_full[qs], static_cast<uint32_t>(piece / C::kQSlots) & 1u, ctx, kWhereFull)) break;
       q_off = C::kQOffset + qs * C::kQSlot;
       const uint2 *qsm = reinterpret_cast<const uint2 *>(smem + q_off) + lane;
       const float *qscale = reinterpret_cast<const float *>(smem + q_off + (D / 16) * NT * 32 * 8);
@@ -660,10 +700,6 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             qf[kk][nt][1] = f.y;
           }
         }
-      }
-      if constexpr (!C::kQInSmem) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&q_free[qs]);
       }
 #pragma unroll
       for (int dm = 0; dm < D / 16; ++dm)
@@ -868,10 +904,6 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       continue;
     }
     // ---- a piece ends: leave the warp's state in the stage ----
-    if constexpr (C::kQInSmem) {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&q_free[piece & 1]);
-    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
