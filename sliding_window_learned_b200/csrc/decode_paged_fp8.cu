@@ -39,16 +39,18 @@
 //              states at the end of a piece while the consumers go on.
 //
 // Bound by HBM at long contexts: D + 1 bytes per key, kv head and K or V.  64
-// sequences of 4 K..131 K keys, Hq32 Hkv4 D128, 256-position pages: 643 us, 7.2
-// TB/s (1.10 of the measured copy rate, which reads and writes); 8 of them 110 us,
-// 6.1 TB/s, where the start (2.5 us to the first copies, then every CTA's first
+// sequences of 4 K..131 K keys, Hq32 Hkv4 D128, 256-position pages: 640 us, 7.2
+// TB/s (1.10 of the measured copy rate, which reads and writes); 8 of them 108 us,
+// 6.2 TB/s, where the start (2 us to the first copies, then every CTA's first
 // stages at once) and the end show.  With 16 heads a group the consumers' chain of
-// dependent instructions bounds it: 5.3 TB/s.  Tried and dropped: K's codes straight
-// into e4m3 MMAs with q as two e4m3 terms (a quarter fewer instructions, but those
-// MMAs' latency is longer: 643 -> 720 us, 16 heads 503 -> 667); the consumers as
-// two groups that take tiles in turn with two key blocks a warp (110 -> 113 us, D =
-// 64 204 -> 304); one producer warp (its lanes' TMA copies are issued one after
-// another: pages of 16 positions 119 us against 74).
+// dependent instructions bounds it: 5.6 TB/s.  Tried and dropped, each against the
+// version it was tried on: K's codes straight into e4m3 MMAs with q as two e4m3
+// terms (a quarter fewer instructions, but those MMAs' latency is longer: 643 ->
+// 720 us, 16 heads 503 -> 667); the consumers as two groups that take tiles in turn
+// with two key blocks a warp (110 -> 113 us, D = 64 204 -> 304); one producer warp
+// (its lanes' TMA copies are issued one after another: pages of 16 positions 119 us
+// against 74); the merge as a function of its own (its spills cost 2.4 us of launch
+// time).
 #include <math.h>
 
 #include <type_traits>
@@ -110,9 +112,11 @@ Workspace layout(const PagedFp8Args &a, int teams) {
 }
 
 // Where no sequence can have more tiles than this (a short window or a short
-// table), nothing is cut: an item is a sequence's kv head, there is no plan and no
-// combine launch.  One sequence in a window of 513, 4 kv heads, D = 128 (three
-// tiles): 10.1 us, cut and combined 11.4; 64 of them 17.4 us against 22.7.
+// table), nothing is cut: an item is a sequence's kv head, there is no plan, no
+// workspace and no combine launch.  4 kv heads, D = 128, whole against cut: one
+// sequence in a window of 513 (three tiles) 8.7 and 9.6 us, 64 of them 15.5 and
+// 19.2; at seven tiles (a window of 1300) it turns with the batch: two sequences
+// 12.3 and 11.1, sixteen 13.4 and 14.9.
 constexpr int kWholeTiles = 4;
 constexpr int tile_keys(int D) { return D == 64 ? 384 : D == 128 ? 192 : 128; }
 bool takes_whole(const PagedFp8Args &a) {
@@ -468,8 +472,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
           qsm[(kk * NT + nt) * 32] = make_uint2(f32x2_to_f16x2(qx[nt][kk][0], sc), f32x2_to_f16x2(qx[nt][kk][1], sc));
+        // (never 0, which would make NaN of a masked key's -infinity)
         if ((lane & 3) == 0)
-          qscale[nt * 8 + (lane >> 2)] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+          qscale[nt * 8 + (lane >> 2)] =
+              fmaxf(p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23), __uint_as_float(1u));
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[qs]);

@@ -292,6 +292,18 @@ def test_decode_extremes(kind):
     assert (np.abs(got - ref) <= _tol(ref, mag, top, 500, D)).all(), np.abs(got - ref).max()
 
 
+@pytest.mark.parametrize("scale", [1e-9, 0.0883, 1e-38])
+def test_decode_queries_of_zeros_and_tiny_ones(scale):
+    """A head of zeros weighs every visible key alike, whatever the scale, beside masked keys too."""
+    seqlens, MP, P, Hkv, G, D, W = [500, 70, 1], 8, 64, 2, 4, 128, 333
+    c = list(_decode_case(25, seqlens, MP, P, Hkv, G, D, W))
+    c[0][:, 0::4] = 0
+    c[0][:, 1::4] = c[0][:, 1::4] * 2.0 ** -118
+    ref, mag, top = cache8.decode(inputs.bits(c[0]), *c[1:], W, scale)
+    got = _decode(*c, W, scale)
+    assert (np.abs(got - ref) <= _tol(ref, mag, top, 500, D)).all(), np.abs(got - ref).max()
+
+
 def test_decode_nan_of_a_visible_row_reaches_its_heads_only():
     seqlens, MP, P, Hkv, G, D, W = [300, 90], 5, 64, 2, 4, 64, 1 << 30
     c = _decode_case(23, seqlens, MP, P, Hkv, G, D, W)
