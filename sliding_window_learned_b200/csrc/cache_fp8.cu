@@ -215,6 +215,8 @@ template <int D, int kUnroll>
 __global__ void __launch_bounds__(kThreads, kAppendBlocks) cache_append_kernel(const CacheArgs a) {
   using C = Cfg<D, kUnroll>;
   __shared__ int stage[2 * kStageB + 1];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
   Walk w = begin<C::kStep>(a, stage);
   __syncthreads();
   const int lane = threadIdx.x & 31, part = lane % C::kLanes, sub = lane / C::kLanes;
@@ -284,6 +286,8 @@ template <int D, int kUnroll>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheArgs a) {
   using C = Cfg<D, kUnroll>;
   __shared__ int stage[2 * kStageB + 1];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
   Walk w = begin<C::kStep>(a, stage);
   __syncthreads();
   const int lane = threadIdx.x & 31, part = lane % C::kLanes, sub = lane / C::kLanes;
@@ -343,8 +347,18 @@ cudaError_t launch_unrolled(CacheArgs a, bool append, int blocks_per_sm, int sms
   a.stride_rows = a.stride / a.Hkv;
   a.stride_heads = static_cast<int>(a.stride - a.stride_rows * a.Hkv);
   a.hkv_inv = a.Hkv == 1 ? 0 : static_cast<uint32_t>(0x100000000ull / static_cast<uint64_t>(a.Hkv) + 1);
-  kern<<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  // (launched with programmatic dependence, as the decode that may follow: its
+  // blocks come up while the kernel before it ends)
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
 template <int D>

@@ -257,11 +257,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     paged_fp8_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                            const __grid_constant__ Params p) {
   using C = Cfg<D, NT>;
-  asm volatile("griddepcontrol.launch_dependents;");
   // (128-byte swizzled boxes need 1024-byte aligned addresses; aligning by hand
   // would hide from the compiler that this is shared memory)
   extern __shared__ __align__(1024) uint8_t smem[];
   if (reinterpret_cast<uintptr_t>(smem) & 1023u) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (threadIdx.x == 0) report_launch_error(p.a.status, kWhereAlign);
     return;
   }
@@ -294,6 +294,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
+  // (what the launch overlaps ends here; the combine may start from here on)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
 
   if (warp >= C::kCW) {
     // ------------------------------------------------------------- producers
@@ -1060,18 +1063,21 @@ cudaError_t launch(const Params &p, int sms, cudaStream_t stream) {
   if ((e = cudaFuncSetAttribute(split, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes)) != cudaSuccess)
     return e;
   const int64_t items = p.whole ? static_cast<int64_t>(a.B) * a.Hkv : static_cast<int64_t>(p.teams) * a.Hkv;
-  split<<<static_cast<unsigned>(items < sms ? items : sms), C::kThreads, C::kSmemBytes, stream>>>(mk, mv, p);
-  if ((e = cudaGetLastError()) != cudaSuccess || p.whole) return e;
-  const int64_t warps = static_cast<int64_t>(p.teams) * a.Hq + (a.B + 31) / 32;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((warps + 3) / 4));
-  cfg.blockDim = dim3(128);
-  cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(items < sms ? items : sms));
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  if ((e = cudaLaunchKernelEx(&cfg, split, mk, mv, p)) != cudaSuccess || p.whole) return e;
+  const int64_t warps = static_cast<int64_t>(p.teams) * a.Hq + (a.B + 31) / 32;
+  cfg.gridDim = dim3(static_cast<unsigned>((warps + 3) / 4));
+  cfg.blockDim = dim3(128);
+  cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, paged_fp8_combine_kernel<D>, p);
 }
 
