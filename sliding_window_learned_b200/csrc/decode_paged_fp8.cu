@@ -19,7 +19,8 @@
 //            heads of the same positions (whole DRAM bursts).  A span may
 //            end one sequence and begin others; a sequence that lies in one span
 //            is finished there (sink included), one that is cut leaves a partial
-//            (O_s, LSE_s) per span.
+//            (O_s, LSE_s) per span.  Launched with programmatic dependence too:
+//            its CTAs set up while the kernel before them ends.
 //   combine  merges the spans of each cut sequence, in order, and adds the sink
 //            once; writes zeros for empty sequences.  Launched with programmatic
 //            dependence: its blocks are resident before the split ends.
@@ -113,9 +114,9 @@ Workspace layout(const PagedFp8Args &a, int teams) {
 
 // Where no sequence can have more tiles than this (a short window or a short
 // table), nothing is cut: an item is a sequence's kv head, there is no plan, no
-// workspace and no combine launch.  4 kv heads, D = 128, whole against cut: one
-// sequence in a window of 513 (three tiles) 8.7 and 9.6 us, 64 of them 15.5 and
-// 19.2; at seven tiles (a window of 1300) it turns with the batch: two sequences
+// workspace and no combine launch.  4 kv heads, D = 128, whole against cut (both
+// before the overlapped start, which takes 0.6 us off either): one sequence in a
+// window of 513 (three tiles) 8.7 and 9.6 us, 64 of them 15.5 and 19.2; at seven tiles (a window of 1300) it turns with the batch: two sequences
 // 12.3 and 11.1, sixteen 13.4 and 14.9.
 constexpr int kWholeTiles = 4;
 constexpr int tile_keys(int D) { return D == 64 ? 384 : D == 128 ? 192 : 128; }
@@ -294,7 +295,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  // (what the launch overlaps ends here; the combine may start from here on)
+  // (what may overlap the kernel before it ends here, 0.6 us of a short call; the
+  // combine may start from here on)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
 

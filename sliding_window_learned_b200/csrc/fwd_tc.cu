@@ -395,6 +395,7 @@ __global__ void __launch_bounds__(Cfg<D, BN, NH>::kThreads, Cfg<D, BN, NH>::kCta
   // has no slack for aligning by hand, so a base off the declared alignment
   // is reported and nothing runs)
   if (reinterpret_cast<uintptr_t>(smem_raw) & 1023u) {
+    if constexpr (kPrior) asm volatile("griddepcontrol.wait;" ::: "memory");
     if (threadIdx.x == 0) report_launch_error(p.status, kWhereAlign);
     return;
   }
@@ -511,6 +512,9 @@ __global__ void __launch_bounds__(Cfg<D, BN, NH>::kThreads, Cfg<D, BN, NH>::kCta
     tc_fence_after();
     tmem = *tmem_slot;
   }
+  // (kPrior is launched with programmatic dependence: what may overlap the kernel
+  // before it ends here.  8 short chunks after up to 300 keys: 9.4 us, 10.5 without)
+  if constexpr (kPrior) asm volatile("griddepcontrol.wait;" ::: "memory");
 
   if (warp >= C::kSoftmaxWarps) {
   if (warp == C::kProducerWarp) {
@@ -1075,17 +1079,24 @@ cudaError_t launch(const FwdArgs &a, cudaStream_t stream) {
   const int sms = (dev >= 0 && dev < 64) ? sm_count[dev] : 148;
   const int slots = sms * C::kCtasPerSm;
   dim3 grid(p.num_units < slots ? p.num_units : slots);
-  kern<<<grid, C::kThreads, C::kSmemBytes, stream>>>(mq, mk, mv, mo, p);
-  if ((e = cudaGetLastError()) != cudaSuccess || p.nsplit == 1) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.num_units / p.nsplit), kBM / kCombineRows);
-  cfg.blockDim = dim3(kCombineRows * 32);
-  cfg.stream = stream;
+  if (!kPrior) {
+    kern<<<grid, C::kThreads, C::kSmemBytes, stream>>>(mq, mk, mv, mo, p);
+    return cudaGetLastError();
+  }
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  if ((e = cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, mo, p)) != cudaSuccess || p.nsplit == 1) return e;
+  cfg.gridDim = dim3(static_cast<unsigned>(p.num_units / p.nsplit), kBM / kCombineRows);
+  cfg.blockDim = dim3(kCombineRows * 32);
+  cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, prior_combine_kernel<D, BN>, p);
 }
 

@@ -388,6 +388,64 @@ def test_calls_on_two_streams_and_threads_at_once():
     assert swl.attn_sink_get_status() == 0
 
 
+@pytest.mark.parametrize("W", [100, 1 << 30])
+@pytest.mark.parametrize("captured", [False, True])
+def test_calls_follow_the_kernels_before_them(W, captured):
+    """Kernels that come up while the one before them ends read and write only behind it: every
+    step's inputs are written by a kernel just before its calls, its outputs read just behind
+    them, twenty steps in a row without a wait (W = 100: one launch a decode; else two)."""
+    B, Hkv, G, D, P, MP, steps = 3, 2, 4, 128, 64, 30, 20
+    g = torch.Generator().manual_seed(91)
+    rnd = lambda *s: torch.randn(*s, generator=g).bfloat16().to(DEV)  # noqa: E731
+    table = torch.randperm(B * MP, generator=g).reshape(B, MP).int().to(DEV)
+    sinks = torch.zeros(Hkv * G, device=DEV)
+    new = 5                                            # rows of every sequence in a step
+    cu = _i32(np.arange(B + 1) * new)
+    qs, ks, vs = rnd(steps, B, Hkv * G, D), rnd(steps, B * new, Hkv, D), rnd(steps, B * new, Hkv, D)
+    lens = torch.tensor([[1800 + 5 * t, 70 + 5 * t, 5 + 5 * t] for t in range(steps)], dtype=torch.int32, device=DEV)
+    first = _pools(*_random_pools(np.random.default_rng(92), B * MP, P, Hkv, D))
+    q, k, v, sl = qs[0].clone(), ks[0].clone(), vs[0].clone(), lens[0].clone()
+    out, kb, vb, ext = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v), rnd(B * new, Hkv * G, D)
+    q2 = rnd(B * new, Hkv * G, D)
+
+    def serve(pools, wait):
+        """All steps' outputs."""
+        res = []
+        for t in range(steps):
+            for x, y in ((q, qs), (k, ks), (v, vs), (sl, lens)):
+                x.copy_(y[t])
+            for call in (lambda: swl.attn_sink_cache_append_fp8(k, v, table, sl, cu, *pools),
+                         lambda: swl.attn_sink_decode_paged_fp8(q, *pools, table, sl, sinks, W, 0.09, out),
+                         lambda: swl.attn_sink_cache_read_fp8(*pools, table, sl, cu, kb, vb),
+                         lambda: swl.attn_sink_fwd_extend(q2, kb, vb, cu, cu, new, sinks, W, 0.09, ext)):
+                if wait:
+                    torch.cuda.synchronize()
+                call()
+            if wait:
+                torch.cuda.synchronize()
+            res.append([x.clone() for x in (out, kb, vb, ext)])
+            for x in (out, kb, vb, ext):
+                x.fill_(7)
+        return res
+
+    clone = lambda: [x.view(torch.uint8).clone().view(x.dtype) for x in first]  # noqa: E731
+    want = serve(clone(), True)
+    pools = clone()
+    if captured:
+        serve(clone(), False)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = serve(pools, False)
+        graph.replay()
+    else:
+        got = serve(pools, False)
+    torch.cuda.synchronize()
+    assert swl.attn_sink_get_status() == 0
+    for t in range(steps):
+        for a, b in zip(got[t], want[t]):
+            assert torch.equal(a, b), t
+
+
 def test_decode_empty_table_and_batch():
     c = _decode_case(27, [0, 0], 1, 16, 1, 2, 64, 5)
     out = torch.full((2, 2, 64), 5.0, dtype=torch.bfloat16, device=DEV)
