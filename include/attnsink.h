@@ -162,6 +162,8 @@ int attn_sink_fwd_varlen(const attn_tensor *q, const attn_tensor *k, const attn_
  * LSE = its sink.  Rows of q outside every sequence are left as they are in out
  * and lse.  A NaN or infinity in a value row can reach queries of its own
  * sequence that do not see it (never another sequence's).
+ * The softmax's weights go into the product with V as bf16 (as two bf16 terms where
+ * T * Hq <= 512: few roundings do not average).
  * Supported head dims D: 64, 128, 256.  B = 0, T = 0 or max_seqlen_q = 0 is a
  * no-op.  Runs on the tcgen05/TMEM tensor-core kernel of attn_sink_fwd.
  */

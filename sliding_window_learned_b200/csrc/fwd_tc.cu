@@ -223,8 +223,9 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 
 // P = 2^(S*scale*log2e - m_use) for one row tile held in registers (sv),
 // written as bf16 over the first BN/2 columns at p_addr; returns the fp32 sum
-// of P, and with kMax also the tile's raw maximum in tmax.
-template <int BN, bool kMax>
+// of P, and with kMax also the tile's raw maximum in tmax.  With kTwo what the
+// rounding leaves of P follows, as bf16, in the columns behind.
+template <int BN, bool kMax, bool kTwo>
 __device__ __forceinline__ float exp_tile(const uint32_t (&sv)[BN / 32][32], uint32_t p_addr,
                                           float sl2, float m_use, uint32_t cls_none, float &tmax) {
   const uint64_t sl2x2 = f2pack(sl2, sl2);
@@ -234,10 +235,13 @@ __device__ __forceinline__ float exp_tile(const uint32_t (&sv)[BN / 32][32], uin
   float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
   for (int c = 0; c < BN / 32; ++c) {
-    uint32_t pk[16];
+    uint32_t pk[16], rest[kTwo ? 16 : 1];
     if (cls_none >> c & 1u) {
 #pragma unroll
-      for (int t = 0; t < 16; ++t) pk[t] = 0u;
+      for (int t = 0; t < 16; ++t) {
+        pk[t] = 0u;
+        if constexpr (kTwo) rest[t] = 0u;
+      }
     } else {
 #pragma unroll
       for (int t = 0; t < 16; ++t) {
@@ -258,9 +262,12 @@ __device__ __forceinline__ float exp_tile(const uint32_t (&sv)[BN / 32][32], uin
           accs[(t + 2) & 3] += p1;
         }
         pk[t] = pack_bf16x2(p0, p1);
+        if constexpr (kTwo)
+          rest[t] = pack_bf16x2(p0 - __uint_as_float(pk[t] << 16), p1 - __uint_as_float(pk[t] & 0xFFFF0000u));
       }
     }
     tmem_st16(p_addr + c * 16, pk);
+    if constexpr (kTwo) tmem_st16(p_addr + BN / 2 + c * 16, rest);
   }
   if (kMax) tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
   if (kPackedAdd) {
@@ -295,7 +302,7 @@ __device__ __forceinline__ float tile_max(const uint32_t (&sv)[BN / 32][32], uin
 // maximum then grew by more than the lazy-rescale threshold (rare after the
 // first tiles) does its warp rescale O and recompute P.  Returns false if a
 // bounded wait ran out.
-template <int D, int BN>
+template <int D, int BN, bool kTwo>
 __device__ __forceinline__ bool softmax_tile(uint32_t lane_base, uint32_t s_col, uint32_t o_col,
                                              int j, int g, float sl2, int lo, int hi, uint32_t cls_mask,
                                              uint32_t cls_none, float &m_run, float &l_run,
@@ -317,11 +324,11 @@ __device__ __forceinline__ bool softmax_tile(uint32_t lane_base, uint32_t s_col,
     const float mt2 = tile_max<BN>(sv, cls_none) * sl2;
     row_max = fmaxf(row_max, mt2);
     if (mt2 > m_run + kRescaleThreshold) m_run = mt2;
-    l_run = exp_tile<BN, false>(sv, lane_base + s_col, sl2, (m_run == -INFINITY) ? 0.f : m_run,
+    l_run = exp_tile<BN, false, kTwo>(sv, lane_base + s_col, sl2, (m_run == -INFINITY) ? 0.f : m_run,
                                 cls_none, tm);
     return true;
   }
-  const float sum = exp_tile<BN, kFusedMax>(sv, lane_base + s_col, sl2,
+  const float sum = exp_tile<BN, kFusedMax, kTwo>(sv, lane_base + s_col, sl2,
                                             (m_run == -INFINITY) ? 0.f : m_run, cls_none, tm);
   // Without the fused maximum: every P <= 2^threshold when the tile's sum is
   // at most that, so no row can have moved past the threshold; otherwise the
@@ -355,7 +362,7 @@ __device__ __forceinline__ bool softmax_tile(uint32_t lane_base, uint32_t s_col,
     tmem_st32(lane_base + o_col + c * 32, o);
   }
   tmem_wait_st();
-  l_run = l_run * alpha + exp_tile<BN, false>(sv, lane_base + s_col, sl2,
+  l_run = l_run * alpha + exp_tile<BN, false, kTwo>(sv, lane_base + s_col, sl2,
                                               (m_run == -INFINITY) ? 0.f : m_run, cls_none, tm);
   return true;
 }
@@ -384,7 +391,7 @@ __device__ __forceinline__ void atomic_max_float(float *addr, float v) {
 // that a chunk of few tokens fills them, and their keys may be split.
 // kMaxLogit: also the largest content logit scale*<q_i,k_j> over every row and
 // visible key of each (sequence, head), into Params::max_logit (atomic max).
-template <int D, int BN, int NH, bool kPacked, bool kMaxLogit, bool kPrior>
+template <int D, int BN, int NH, bool kPacked, bool kMaxLogit, bool kPrior, bool kTwo>
 __global__ void __launch_bounds__(Cfg<D, BN, NH>::kThreads, Cfg<D, BN, NH>::kCtasPerSm)
     fwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
@@ -641,6 +648,11 @@ __global__ void __launch_bounds__(Cfg<D, BN, NH>::kThreads, Cfg<D, BN, NH>::kCta
         for (int kk = 0; kk < BN / 16; ++kk)
           umma_ts_w(d, a0 + kk * 8, b0 + kk * (16 * 128 >> 4), desc_hi, idesc_pv,
                     (j > 0 || kk > 0) ? 1u : 0u);
+        if constexpr (kTwo) {
+#pragma unroll
+          for (int kk = 0; kk < BN / 16; ++kk)
+            umma_ts_w(d, a0 + BN / 2 + kk * 8, b0 + kk * (16 * 128 >> 4), desc_hi, idesc_pv, 1u);
+        }
         umma_commit(&pv_done[w]);
       };
       int jg = 0;                            // tiles of earlier units (barrier phases)
@@ -759,8 +771,8 @@ __global__ void __launch_bounds__(Cfg<D, BN, NH>::kThreads, Cfg<D, BN, NH>::kCta
             cls_mask |= (!all_in && !all_out ? 1u : 0u) << c;
           }
         }
-        if (!softmax_tile<D, BN>(lane_base, s_col, o_col, j, g, sl2, lo, hi, cls_mask, cls_none,
-                                 m_run, l_run, row_max, &pv_done[w], ctx)) {
+        if (!softmax_tile<D, BN, kTwo>(lane_base, s_col, o_col, j, g, sl2, lo, hi, cls_mask, cls_none,
+                                       m_run, l_run, row_max, &pv_done[w], ctx)) {
           ok = false;
           break;
         }
@@ -1002,7 +1014,16 @@ int prior_splits(const FwdArgs &a, int ctas_per_sm, int sms) {
   return n < 2 ? 1 : static_cast<int>(n);
 }
 
-template <int D, int BN, int NH, bool kPacked, bool kMaxLogit = false, bool kPrior = false>
+// Whether P goes into a kPrior product as two bf16 terms, 2^-16 of it off instead of
+// 2^-8.  One term's error is about that of the bf16 output (together 1.4 times the
+// output's own); over many rows it averages to that, but a call of few rows can have
+// 1.6 times.  Such calls wait for memory and launches, and two terms cost them 5..12 %
+// (3 queries of 12 heads after 1 K keys 14.5 -> 15.7 us); a call that fills the
+// machine would pay 13..29 % (4096 queries after 12 K keys 960 -> 1235 us).
+constexpr int kTwoTermRows = 512;
+bool prior_two_terms(const FwdArgs &a) { return static_cast<int64_t>(a.T) * a.Hq <= kTwoTermRows; }
+
+template <int D, int BN, int NH, bool kPacked, bool kMaxLogit = false, bool kPrior = false, bool kTwo = false>
 cudaError_t launch(const FwdArgs &a, cudaStream_t stream) {
   using C = Cfg<D, BN, NH>;
   alignas(64) CUtensorMap mq, mk, mv, mo;
@@ -1062,7 +1083,7 @@ cudaError_t launch(const FwdArgs &a, cudaStream_t stream) {
     // every entry starts at -inf; the kernel's units raise it
     if ((e = launch_max_logit_init(a.max_logit, a.ml_sb, a.B, a.Hq, stream)) != cudaSuccess) return e;
   }
-  auto kern = fwd_tc_kernel<D, BN, NH, kPacked, kMaxLogit, kPrior>;
+  auto kern = fwd_tc_kernel<D, BN, NH, kPacked, kMaxLogit, kPrior, kTwo>;
   static bool attr_set[64] = {};  // once per device (per instantiation)
   int dev = 0;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
@@ -1124,6 +1145,14 @@ cudaError_t launch_fwd_tc(const FwdArgs &a, cudaStream_t stream) {
   const bool ml = a.max_logit != nullptr;   // (batched inputs only)
   if (packed && ml) return cudaErrorInvalidValue;
   if (a.cu_seqlens_k != nullptr) {
+    if (prior_two_terms(a)) {
+      switch (a.D) {
+        case 64: return launch<64, 64, 1, true, false, true, true>(a, stream);
+        case 128: return launch<128, 64, 1, true, false, true, true>(a, stream);
+        case 256: return launch<256, 64, 1, true, false, true, true>(a, stream);
+        default: return cudaErrorInvalidValue;
+      }
+    }
     switch (a.D) {
       case 64: return launch<64, 64, 1, true, false, true>(a, stream);
       case 128: return launch<128, 64, 1, true, false, true>(a, stream);

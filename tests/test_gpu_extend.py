@@ -102,6 +102,22 @@ def test_extend_against_the_definition(case):
     assert (o[T:] == 9.0).all() and (lse[:, T:] == 9.0).all(), "rows of no sequence were written"
 
 
+@pytest.mark.parametrize("lq,lk,Hkv,G,D,W", [
+    ([1], [9], 1, 1, 64, 1 << 30), ([3, 1], [1000, 70], 1, 16, 128, 513), ([2, 2, 0, 3], [2, 300, 5, 65], 2, 5, 256, 100),
+    ([16], [4000], 2, 8, 128, 1 << 30), ([5, 1], [3, 200], 1, 2, 64, 1 << 30), ([1] * 8, [2900] * 8, 4, 8, 64, 1 << 30)])
+def test_extend_of_few_rows_rounds_the_weights_twice(lq, lk, Hkv, G, D, W):
+    """At most 512 rows: P as two bf16 terms, 2^-16 off (2^-8 the rest, and 2^-8 of that)."""
+    q, k, v, cu_q, cu_k, sinks = _case(60, lq, lk, Hkv, G, D, tail=(0, 5))
+    assert q.shape[0] * Hkv * G <= 512
+    ro, rl, mag, top = cache8.extend(q=inputs.bits(q), k=inputs.bits(k), v=inputs.bits(v), cu_q=cu_q, cu_k=cu_k,
+                                     sinks=sinks, window=W, scale=D ** -0.5)
+    o, lse = _run(q, k, v, cu_q, cu_k, sinks, W, D ** -0.5)
+    n = min(W, max(lk))
+    tol = _tol(ro, mag, top, n, D) - (2.0 ** -8 - 2.0 ** -16) * mag * 1.01
+    assert (np.abs(o - ro) <= tol).all(), (np.abs(o - ro) / tol).max()
+    assert (np.abs(lse - rl) <= _tol_lse(rl, top, n, D)).all()
+
+
 @pytest.mark.parametrize("G", [1, 3])
 def test_extend_without_earlier_keys_is_the_packed_forward(G):
     q, k, v, cu, _, sinks = _case(50, [200, 1, 77], [200, 1, 77], 2, G, 128, tail=(0, 0))
