@@ -446,6 +446,59 @@ def test_calls_follow_the_kernels_before_them(W, captured):
             assert torch.equal(a, b), t
 
 
+@pytest.mark.parametrize("captured", [False, True])
+def test_calls_behind_two_streams(captured):
+    """The kernels before a call are on two streams that join just before it."""
+    B, Hkv, G, D, P, MP = 2, 2, 4, 128, 64, 20
+    c = _decode_case(93, [1200, 600], MP, P, Hkv, G, D, 1 << 30)
+    first, table, sinks = _pools(*c[1:5]), _i32(c[5]), torch.from_numpy(c[7]).to(DEV)
+    sl, q0 = _i32(c[6]), c[0].to(DEV)
+    k0, v0 = (torch.randn(B, Hkv, D, device=DEV).bfloat16() for _ in range(2))
+    cu = _i32([0, 1, 2])
+    junk, big = torch.randn(2500, 2500, device=DEV), torch.empty(2500, 2500, device=DEV)
+    q, k, v, out = (torch.zeros_like(x) for x in (q0, k0, v0, q0))
+    kb, vb, ext = torch.zeros_like(k), torch.zeros_like(v), torch.zeros(B, Hkv * G, D, dtype=torch.bfloat16, device=DEV)
+    side = torch.cuda.Stream()
+
+    def step(pools, wait=lambda: None):
+        main = torch.cuda.current_stream()
+        for call, slow, fast in (
+                (lambda: swl.attn_sink_cache_append_fp8(k, v, table, sl, cu, *pools), (k, k0), (v, v0)),
+                (lambda: swl.attn_sink_decode_paged_fp8(q, *pools, table, sl, sinks, 1 << 30, 0.09, out), (q, q0), (k, k0)),
+                (lambda: swl.attn_sink_decode_paged_fp8(q, *pools, table, sl, sinks, 30, 0.09, ext), (q, 0.5 * q0), (k, k0)),
+                (lambda: swl.attn_sink_cache_read_fp8(*pools, table, sl, cu, kb, vb), (kb, 2 * k0), (vb, v0)),
+                (lambda: swl.attn_sink_fwd_extend(q, kb, vb, cu, cu, 1, sinks, 9, 0.09, ext), (q, q0), (vb, 3 * v0))):
+            side.wait_stream(main)
+            with torch.cuda.stream(side):              # the slower stream writes an input last
+                torch.mm(junk, junk, out=big)
+                torch.add(slow[1], big[0, 0] * 0, out=slow[0])
+            torch.mul(fast[1], 1, out=fast[0])
+            main.wait_stream(side)
+            wait()
+            call()
+            wait()
+
+    clone = lambda: [x.view(torch.uint8).clone().view(x.dtype) for x in first]  # noqa: E731
+    res = (out, kb, vb, ext)
+    pools = clone()
+    step(pools, torch.cuda.synchronize)
+    want = [x.clone() for x in res] + [x.view(torch.uint8).clone() for x in pools]
+    pools = clone()
+    for x in (q, k, v, *res):
+        x.zero_()
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step(pools)
+        graph.replay()
+    else:
+        step(pools)
+    torch.cuda.synchronize()
+    assert swl.attn_sink_get_status() == 0
+    for a, b in zip(list(res) + [x.view(torch.uint8) for x in pools], want):
+        assert torch.equal(a, b)
+
+
 def test_decode_empty_table_and_batch():
     c = _decode_case(27, [0, 0], 1, 16, 1, 2, 64, 5)
     out = torch.full((2, 2, 64), 5.0, dtype=torch.bfloat16, device=DEV)
