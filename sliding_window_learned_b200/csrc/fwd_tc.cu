@@ -134,7 +134,7 @@ struct Params {
   // its keys go to `nsplit` units, whose partial O (f32, normalised) and log2-sums
   // lie in o_part [units][128][D] and lse_part [units][128] when nsplit > 1.
   const int *cu_seqlens_k;
-  int Tk, pack, ppt, nsplit;
+  int Tk, pack, ppt, nsplit, early;
   float *o_part, *lse_part;
 };
 
@@ -405,6 +405,13 @@ __global__ void __launch_bounds__(Cfg<D, BN, NH>::kThreads, Cfg<D, BN, NH>::kCta
     if constexpr (kPrior) asm volatile("griddepcontrol.wait;" ::: "memory");
     if (threadIdx.x == 0) report_launch_error(p.status, kWhereAlign);
     return;
+  }
+  // (a grid on at most half the SMs, with no merge behind it: the next kernel may come
+  // up at once.  Three queries after 30 keys 6.6 -> 5.8 us a call; with more SMs taken
+  // its CTAs crowd where this one's end first: 30 single queries, 120 CTAs, 18.9 ->
+  // 19.9 us, 4 windowed chunks 57 -> 59)
+  if constexpr (kPrior) {
+    if (p.early) asm volatile("griddepcontrol.launch_dependents;");
   }
   uint8_t *smem = smem_raw;
   uint8_t *sQ = smem;                       // [2] units' Q tiles, later their O staging
@@ -963,9 +970,11 @@ __global__ void __launch_bounds__(kCombineRows * 32) prior_combine_kernel(const 
     for (int s = 0; s < kAhead; ++s)
 #pragma unroll
       for (int c = 0; c < kPer / 2; ++c) {
-        v[s][c] = make_float2(0.f, 0.f);            // (a split without a tile wrote nothing)
-        if (have >> (s0 + s) & 1u)
-          v[s][c] = *reinterpret_cast<const float2 *>(po + static_cast<int64_t>(s0 + s) * kBM * D + 2 * c);
+        // (loaded whatever it is, so that the loads do not wait for the log-sums: a
+        // split without a tile wrote nothing)
+        const float2 x = *reinterpret_cast<const float2 *>(
+            po + static_cast<int64_t>(min(s0 + s, p.nsplit - 1)) * kBM * D + 2 * c);
+        v[s][c] = have >> (s0 + s) & 1u ? x : make_float2(0.f, 0.f);
       }
 #pragma unroll
     for (int s = 0; s < kAhead; ++s) {
@@ -1099,6 +1108,7 @@ cudaError_t launch(const FwdArgs &a, cudaStream_t stream) {
       return e;
   const int sms = (dev >= 0 && dev < 64) ? sm_count[dev] : 148;
   const int slots = sms * C::kCtasPerSm;
+  p.early = kPrior && p.nsplit == 1 && 2 * p.num_units <= sms;
   dim3 grid(p.num_units < slots ? p.num_units : slots);
   if (!kPrior) {
     kern<<<grid, C::kThreads, C::kSmemBytes, stream>>>(mq, mk, mv, mo, p);
