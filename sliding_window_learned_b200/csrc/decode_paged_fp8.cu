@@ -545,15 +545,21 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             // (first, so that its latency overlaps the sums; the sink joins here if no
             // other span holds keys of this sequence)
             const float sink2 = u.dest < 0 ? a.sinks[hq] * kLog2e : -INFINITY;
-            float M = kNoMax;
+            float M = kNoMax, N = kNoMax;
 #pragma unroll
-            for (int w = 0; w < C::kCW; ++w) M = fmaxf(M, merge_m[w * 8 + hl]);
+            for (int w = 0; w < C::kCW; ++w) {
+              M = fmaxf(M, merge_m[w * 8 + hl]);
+              N = fmaxf(N, merge_n[w * 8 + hl]);
+            }
+            // the numerator on its own largest reference: 2^(N - M) joins only behind the
+            // division, so that neither the sum of large values nor the weights of small
+            // ones leave f32 where their mean does not
             float den = 0.f;
             float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < C::kCW; ++w) {
               den += merge_l[w * 8 + hl] * ex2_approx(merge_m[w * 8 + hl] - M);
-              const float f = ex2_approx(merge_n[w * 8 + hl] - M);
+              const float f = ex2_approx(merge_n[w * 8 + hl] - N);
               const float4 v = *reinterpret_cast<const float4 *>(mbuf + (w * 8 + hl) * D + (d ^ (hl >> 1 << 3)));
               num.x = fmaf(f, v.x, num.x);
               num.y = fmaf(f, v.y, num.y);
@@ -564,7 +570,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             const float M1 = fmaxf(M, sink2), back = ex2_approx(M - M1);
             den = den * back + ex2_approx(sink2 - M1);
             const float inv = den != 0.f ? back / den : 0.f;
-            num = make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
+            // (in two halves: N - M goes down to -132)
+            const float up = ex2_approx(0.5f * (N - M));
+            num = make_float4(num.x * inv * up * up, num.y * inv * up * up, num.z * inv * up * up, num.w * inv * up * up);
             if (u.dest < 0) {
               __nv_bfloat16 *po = a.out + u.b * a.o_s[0] + hq * a.o_s[1] + d;
               if (p.out8) {
@@ -1021,16 +1029,22 @@ __global__ void __launch_bounds__(128) paged_fp8_combine_kernel(const __grid_con
     M = fmaxf(M, ls);
   }
   const float Mu = M == -INFINITY ? 0.f : M;
-  float den = __expf(sink - Mu);
+  float den = __expf(sink - Mu), wt0 = 0.f;          // wt0: this lane's weight of the first 32 spans
+  for (int i0 = 0; i0 < parts; i0 += 32) {
+    float wt = i0 + lane < parts ? __expf(p.lse_part[slot_of(i0 + lane)] - Mu) : 0.f;
+    if (i0 == 0) wt0 = wt;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) wt += __shfl_xor_sync(0xffffffffu, wt, off);
+    den += wt;
+  }
+  // (divided before the sum: the spans' means may be as large as f32 holds)
+  const float inv = den != 0.f ? 1.f / den : 0.f;
   float acc[kPer];
 #pragma unroll
   for (int t = 0; t < kPer; ++t) acc[t] = 0.f;
   for (int i0 = 0; i0 < parts; i0 += 32) {
-    const float wt = i0 + lane < parts ? __expf(p.lse_part[slot_of(i0 + lane)] - Mu) : 0.f;
-    float sum = wt;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    den += sum;
+    const float wt =
+        inv * (i0 == 0 ? wt0 : i0 + lane < parts ? __expf(p.lse_part[slot_of(i0 + lane)] - Mu) : 0.f);
     const int cnt = min(32, parts - i0);
     int i = 0;
     if (i0 == 0) {
@@ -1049,10 +1063,9 @@ __global__ void __launch_bounds__(128) paged_fp8_combine_kernel(const __grid_con
       for (int t = 0; t < kPer; ++t) acc[t] = fmaf(ws, op[t], acc[t]);
     }
   }
-  const float inv = den != 0.f ? 1.f / den : 0.f;
   __nv_bfloat16 *po = a.out + static_cast<int64_t>(note.x) * a.o_s[0] + hq * a.o_s[1] + lane * kPer;
 #pragma unroll
-  for (int t = 0; t < kPer; ++t) po[t] = __float2bfloat16_rn(acc[t] * inv);
+  for (int t = 0; t < kPer; ++t) po[t] = __float2bfloat16_rn(acc[t]);
 }
 
 template <int D, int NT>

@@ -1,0 +1,80 @@
+"""Decode over the 8-bit pages at the ends of its formats: scales that the append
+may write (2^-117 .. 2^119).  Each case in both forms, sequences finished whole and
+sequences cut over the SMs.  Tolerance as in test_gpu_cache_fp8."""
+import numpy as np
+import pytest
+import torch
+
+import sliding_window_learned_b200 as swl
+from oracle import cache8
+from sliding_window_learned_b200 import inputs
+from test_gpu_cache_fp8 import DEV, _decode, _decode_case, _i32, _pools, _tol
+
+pytestmark = pytest.mark.gpu
+FULL = 1 << 30
+FORMS = {"whole": ([500, 70, 193], 8, 64, 2, 4, 128), "whole, narrow": ([1000, 70], 16, 64, 1, 12, 64),
+         "cut": ([1400, 70, 0, 900], 24, 64, 2, 4, 128),
+         "cut, many parts": ([9000], 141, 64, 1, 2, 64), "cut, wide": ([700, 1, 640], 44, 16, 2, 3, 256)}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from sliding_window_learned_b200 import build
+    build.build()
+
+
+def _check(c, W, scale, n):
+    D = c[0].shape[2]
+    ref, mag, top = cache8.decode(inputs.bits(c[0]), *c[1:], W, scale)
+    got = _decode(*c, W, scale)
+    assert np.isfinite(ref).all() and np.isfinite(got).all()
+    bad = ~(np.abs(got - ref) <= _tol(ref, mag, top, n, D))
+    assert not bad.any(), (np.argwhere(bad)[:3], got[bad][:3], ref[bad][:3])
+    return got
+
+
+@pytest.mark.parametrize("sink", [False, True])
+@pytest.mark.parametrize("form", FORMS)
+def test_the_largest_values(form, sink):
+    """Value rows of up to 448 * 2^119: their sum passes f32, their mean does not."""
+    seqlens, MP, P, Hkv, G, D = FORMS[form]
+    c = list(_decode_case(31, seqlens, MP, P, Hkv, G, D, FULL))
+    c[4] = np.where(c[4] == 255, 255, 246).astype(np.uint8)
+    c[2] &= 0x7F                                           # (one sign: the mean is large)
+    if not sink:
+        c[7][:] = -np.inf
+    got = _check(c, FULL, D ** -0.5, max(seqlens))
+    assert sink or got.max() > 2.0 ** 124
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_the_smallest_values(form):
+    seqlens, MP, P, Hkv, G, D = FORMS[form]
+    c = list(_decode_case(32, seqlens, MP, P, Hkv, G, D, FULL))
+    c[4] = np.where(c[4] == 255, 255, 10).astype(np.uint8)
+    c[7][:] = -np.inf
+    ref, mag, top = cache8.decode(inputs.bits(c[0]), *c[1:], FULL, D ** -0.5)
+    got = _decode(*c, FULL, D ** -0.5)
+    # (bf16's own subnormals start at 2^-126, their half step is 2^-134)
+    assert (np.abs(got - ref) <= _tol(ref, mag, top, max(seqlens), D) - 1e-37 + 2.0 ** -134).all()
+
+
+def test_rows_read_back_at_the_ends_of_the_range_are_the_values_decoded():
+    """Appended rows near bf16's ends, read back and decoded with one key visible: the
+    decode gives that key's values exactly (no sink)."""
+    rng = np.random.default_rng(37)
+    Hkv, D, P = 2, 128, 16
+    T = 16
+    k = torch.zeros(T, Hkv, D, dtype=torch.bfloat16)
+    v = torch.from_numpy(rng.standard_normal((T, Hkv, D)) * 2.0 ** rng.integers(-120, 124, (T, Hkv, 1))).bfloat16()
+    e4, e8 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+    z = lambda *s: torch.zeros(*s, dtype=torch.uint8, device=DEV)  # noqa: E731
+    pools = (z(T, P, Hkv, D).view(e4), z(T, P, Hkv, D).view(e4), z(T, Hkv, P).view(e8), z(T, Hkv, P).view(e8))
+    table, one, cu = _i32(np.arange(T)[:, None]), _i32([1] * T), _i32(np.arange(T + 1))
+    swl.attn_sink_cache_append_fp8(k.to(DEV), v.to(DEV), table, one, cu, *pools)
+    kb, vb = torch.empty(T, Hkv, D, dtype=torch.bfloat16, device=DEV), torch.empty(T, Hkv, D, dtype=torch.bfloat16, device=DEV)
+    swl.attn_sink_cache_read_fp8(*pools, table, one, cu, kb, vb)
+    out = torch.empty(T, Hkv, D, dtype=torch.bfloat16, device=DEV)
+    q = torch.randn(T, Hkv, D, device=DEV).bfloat16()
+    swl.attn_sink_decode_paged_fp8(q, *pools, table, one, torch.full((Hkv,), -float("inf"), device=DEV), 1, 0.1, out)
+    assert torch.equal(out, vb)
