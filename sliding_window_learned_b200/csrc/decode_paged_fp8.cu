@@ -74,6 +74,13 @@ constexpr float kLazy = 8.0f;
 constexpr float kHeadroom = 7.0f;
 constexpr float kNoMax = -1e30f;      // a reference nothing was seen against
 
+// S = K q^T reaches 2^31 (q in f16 up to 2^14), a key's scale 2^119: their product is
+// taken under 2^-24, and the softmax scale, which undoes q's power of two, over it.
+// Logits that fit f32 then pass through no intermediate that does not.  (Where a
+// head's queries are so large, above 2^119, that its softmax scale would overflow,
+// the piece goes without the factor: large keys overflow its logits themselves.)
+constexpr float kDown = 0x1p-24f;
+
 // ------------------------------------------------------------- workspace
 struct Workspace {
   size_t off_info, off_lse, off_o, total;
@@ -185,11 +192,12 @@ struct Cfg {
   static constexpr int kTileBytes = kTK * D;
   static constexpr int kStageBytes = 2 * kTileBytes;        // K then V
   static constexpr int kScaleBytes = 2 * kTK;               // per stage: K then V
-  // a piece's q as B fragments [k-step][head tile][lane] and its heads' scales.
+  // a piece's q as B fragments [k-step][head tile][lane], its heads' scales and kDown's factor.
   // One slot more than stages: when a piece's first tile has its stage, the piece
   // kQSlots before has been released to its last tile, so a slot needs no barrier
   // to say that it is free.
-  static constexpr int kQSlot = (D / 16) * NT * 32 * 8 + NT * 8 * 4;
+  static constexpr int kQScale = (D / 16) * NT * 32 * 8;
+  static constexpr int kQSlot = kQScale + NT * 8 * 4 + 8;
   static constexpr int kQSlots = 5;
   static constexpr int kQBytes = (kQSlots * kQSlot + 127) / 128 * 128;
   static constexpr int kFixed = kQBytes + 3 * kCW * 8 * 4 + 1024;
@@ -459,7 +467,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     };
     auto prepare_q = [&](int qs) {
       uint2 *qsm = reinterpret_cast<uint2 *>(smem + C::kQOffset + qs * C::kQSlot) + lane;
-      float *qscale = reinterpret_cast<float *>(smem + C::kQOffset + qs * C::kQSlot + (D / 16) * NT * 32 * 8);
+      float *qscale = reinterpret_cast<float *>(smem + C::kQOffset + qs * C::kQSlot + C::kQScale);
+      float back[NT];                    // 2^-e of this lane's head
+      bool large = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float mx = 0.f;
@@ -476,14 +486,19 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         const int eb = static_cast<int>(__float_as_uint(mx) >> 23);
         const int e = eb == 255 ? 0 : min(140 - eb, 126);
         const float sc = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+        back[nt] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        large |= isinf(p.scale_log2 * (1.f / kDown) * back[nt]);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
           qsm[(kk * NT + nt) * 32] = make_uint2(f32x2_to_f16x2(qx[nt][kk][0], sc), f32x2_to_f16x2(qx[nt][kk][1], sc));
+      }
+      const float down = __any_sync(0xffffffffu, large) ? 1.f : kDown;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
         // (never 0, which would make NaN of a masked key's -infinity)
         if ((lane & 3) == 0)
-          qscale[nt * 8 + (lane >> 2)] =
-              fmaxf(p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23), __uint_as_float(1u));
-      }
+          qscale[nt * 8 + (lane >> 2)] = fmaxf(p.scale_log2 * (1.f / down) * back[nt], __uint_as_float(1u));
+      if (lane == 0) qscale[NT * 8] = down;
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[qs]);
     };
@@ -703,7 +718,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       if (!warp_wait(&q_full[qs], static_cast<uint32_t>(piece / C::kQSlots) & 1u, ctx, kWhereFull)) break;
       q_off = C::kQOffset + qs * C::kQSlot;
       const uint2 *qsm = reinterpret_cast<const uint2 *>(smem + q_off) + lane;
-      const float *qscale = reinterpret_cast<const float *>(smem + q_off + (D / 16) * NT * 32 * 8);
+      const float *qscale = reinterpret_cast<const float *>(smem + q_off + C::kQScale);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         sl[nt][0] = qscale[nt * 8 + 2 * tig];
@@ -777,6 +792,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       // t = S * kscale; the softmax's exponent is t * sl - M, the numerator's t *
       // sl + ev - m (n_ref is m - headroom): one FMA each.
       float t[KB][NT][4], ev[KB][2];
+      const float down = *reinterpret_cast<const float *>(smem + q_off + C::kQScale + NT * 8 * 4);
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb) {
         const uint8_t *sck = smem + C::kScaleOffset + s * C::kScaleBytes + key_w + kb * 16 + g8;
@@ -784,7 +800,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const uint32_t b = sck[r * 8], vb = sck[C::kTK + r * 8];
-          ks[r] = scale_value(b);
+          ks[r] = scale_value(b) * down;
           // vb - 127 by way of 2^23 + vb, exact
           ev[kb][r] = vb == 255u ? NAN : __uint_as_float(0x4B000000u | vb) - 8388735.f;
         }

@@ -1,6 +1,7 @@
 """Decode over the 8-bit pages at the ends of its formats: scales that the append
-may write (2^-117 .. 2^119).  Each case in both forms, sequences finished whole and
-sequences cut over the SMs.  Tolerance as in test_gpu_cache_fp8."""
+may write (2^-117 .. 2^119) and queries that bring the logits back into range.
+Each case in both forms, sequences finished whole and sequences cut over the SMs.
+Tolerance as in test_gpu_cache_fp8."""
 import numpy as np
 import pytest
 import torch
@@ -57,6 +58,21 @@ def test_the_smallest_values(form):
     got = _decode(*c, FULL, D ** -0.5)
     # (bf16's own subnormals start at 2^-126, their half step is 2^-134)
     assert (np.abs(got - ref) <= _tol(ref, mag, top, max(seqlens), D) - 1e-37 + 2.0 ** -134).all()
+
+
+@pytest.mark.parametrize("key,query,scale", [
+    (246, -121, None), (246, -126, None), (230, -104, None), (10, 116, None), (10, 118, None), (10, 124, 2.0 ** -10),
+    (246, -121, 2.0 ** -3), (246, -110, 2.0 ** -14), (246, -121, 3.0), (60, 40, 2.0 ** 20), (246, -60, 2.0 ** -62)])
+@pytest.mark.parametrize("form", FORMS)
+def test_keys_and_queries_of_opposite_sizes(form, key, query, scale):
+    """Scale bytes at the ends of the append's range, queries that make ordinary logits of them."""
+    seqlens, MP, P, Hkv, G, D = FORMS[form]
+    c = list(_decode_case(33, seqlens, MP, P, Hkv, G, D, FULL))
+    rng = np.random.default_rng(34)
+    low = rng.integers(-3, 1, c[3].shape) if key > 13 else rng.integers(0, 4, c[3].shape)
+    c[3] = np.where(c[3] == 255, 255, key + low).astype(np.uint8)
+    c[0] = torch.from_numpy(rng.standard_normal(c[0].shape) * 2.0 ** (query - 3)).bfloat16()
+    _check(c, FULL, D ** -0.5 if scale is None else scale, max(seqlens))
 
 
 def test_rows_read_back_at_the_ends_of_the_range_are_the_values_decoded():
