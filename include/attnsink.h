@@ -429,8 +429,9 @@ int attn_sink_cache_read_fp8(const attn_tensor *kpages, const attn_tensor *vpage
  * no visible position may hold anything; an entry outside [0, NB) reads as a
  * page of zero rows.  Cache rows outside the window may hold anything, NaN
  * included.  A NaN scale or code of a visible row reaches the outputs of its
- * kv head, and so may a logit that does not fit f32.  Hq/Hkv <= 16 (<= 8 at D = 256;
- * larger groups return ATTN_EUNSUPPORTED).
+ * kv head; a visible logit beyond 2^27 (which f32 rounds by 8 and more) may make its
+ * head's output NaN.  Hq/Hkv <= 16 (<= 8 at D = 256; larger groups return
+ * ATTN_EUNSUPPORTED).
  *
  * Two launches on `stream`, no host synchronisation: the split kernel divides
  * the visible keys of the whole batch evenly over the SMs and finishes every

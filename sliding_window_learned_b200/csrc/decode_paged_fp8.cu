@@ -9,7 +9,8 @@
 // a reference of its own, over y_j = x_j + ev_j, beside the softmax's over x_j:
 //   N = sum_j 2^(y_j - m) cv_j,  L = sum_j 2^(x_j - M),  O = N 2^(m - M) / L.
 // Both references move lazily (only when an exponent would exceed 2^8), which a
-// warp vote decides: the common tile needs no shuffle.
+// warp vote decides: the common tile needs no shuffle.  m is held as m - M: with the
+// two apart, a logit's rounding scaled the output (12 % at logits of 2^20).
 //
 // Two launches, no host synchronisation:
 //   split    persistent, one CTA per SM.  Every CTA reads the lengths and finds
@@ -72,7 +73,7 @@ enum : int { kWhereFull = 401, kWhereEmpty = 402, kWhereMerge = 403, kWhereAlign
 // subnormals as the lazy reference (exponents up to kLazy above it) allows.
 constexpr float kLazy = 8.0f;
 constexpr float kHeadroom = 7.0f;
-constexpr float kNoMax = -1e30f;      // a reference nothing was seen against
+constexpr float kNoMax = -0x1.fffffep127f;   // a reference nothing was seen against: the lowest f32
 
 // S = K q^T reaches 2^31 (q in f16 up to 2^14), a key's scale 2^119: their product is
 // taken under 2^-24, and the softmax scale, which undoes q's power of two, over it.
@@ -285,8 +286,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
   uint64_t *merge_free = merge_full + 1;     // and has been read
   uint64_t *q_full = merge_free + 1;         // [kQSlots] a piece's q is in its slot
   MergeUnit *unit = reinterpret_cast<MergeUnit *>(q_full + C::kQSlots);
-  float *merge_n = reinterpret_cast<float *>(unit + 1);             // numerator reference [kCW][8]
-  float *merge_m = merge_n + C::kCW * 8;                            // softmax reference
+  float *merge_d = reinterpret_cast<float *>(unit + 1);             // numerator reference less the softmax's [kCW][8]
+  float *merge_m = merge_d + C::kCW * 8;                            // softmax reference
   float *merge_l = merge_m + C::kCW * 8;                            // softmax sum
   int *abort_flag = reinterpret_cast<int *>(merge_l + C::kCW * 8);
   const PagedFp8Args &a = p.a;
@@ -560,21 +561,22 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             // (first, so that its latency overlaps the sums; the sink joins here if no
             // other span holds keys of this sequence)
             const float sink2 = u.dest < 0 ? a.sinks[hq] * kLog2e : -INFINITY;
-            float M = kNoMax, N = kNoMax;
+            float M = kNoMax;
 #pragma unroll
-            for (int w = 0; w < C::kCW; ++w) {
-              M = fmaxf(M, merge_m[w * 8 + hl]);
-              N = fmaxf(N, merge_n[w * 8 + hl]);
-            }
-            // the numerator on its own largest reference: 2^(N - M) joins only behind the
+            for (int w = 0; w < C::kCW; ++w) M = fmaxf(M, merge_m[w * 8 + hl]);
+            float N = kNoMax;              // the numerator's reference, less M
+#pragma unroll
+            for (int w = 0; w < C::kCW; ++w) N = fmaxf(N, merge_m[w * 8 + hl] - M + merge_d[w * 8 + hl]);
+            // the numerator on its own largest reference: 2^N joins only behind the
             // division, so that neither the sum of large values nor the weights of small
             // ones leave f32 where their mean does not
             float den = 0.f;
             float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < C::kCW; ++w) {
-              den += merge_l[w * 8 + hl] * ex2_approx(merge_m[w * 8 + hl] - M);
-              const float f = ex2_approx(merge_n[w * 8 + hl] - N);
+              const float below = merge_m[w * 8 + hl] - M;
+              den += merge_l[w * 8 + hl] * ex2_approx(below);
+              const float f = ex2_approx(below + merge_d[w * 8 + hl] - N);
               const float4 v = *reinterpret_cast<const float4 *>(mbuf + (w * 8 + hl) * D + (d ^ (hl >> 1 << 3)));
               num.x = fmaf(f, v.x, num.x);
               num.y = fmaf(f, v.y, num.y);
@@ -585,8 +587,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             const float M1 = fmaxf(M, sink2), back = ex2_approx(M - M1);
             den = den * back + ex2_approx(sink2 - M1);
             const float inv = den != 0.f ? back / den : 0.f;
-            // (in two halves: N - M goes down to -132)
-            const float up = ex2_approx(0.5f * (N - M));
+            // (in two halves: N goes down to -132)
+            const float up = ex2_approx(0.5f * N);
             num = make_float4(num.x * inv * up * up, num.y * inv * up * up, num.z * inv * up * up, num.w * inv * up * up);
             if (u.dest < 0) {
               __nv_bfloat16 *po = a.out + u.b * a.o_s[0] + hq * a.o_s[1] + d;
@@ -701,8 +703,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
   int q_off = 0;                                  // where they are in shared memory
   float o[D / 16][NT][4];                         // O^T accumulators: [d tile][head tile][fragment]
   float sl[NT][2];                                // softmax scale of this lane's heads (with q's power of two)
-  float n_ref[NT][2];                             // numerator reference - headroom (one per head, same in every lane)
-  float m_ref[NT][2], l_run[NT][2];               // softmax reference and sum of this lane's keys
+  // softmax reference and numerator reference (less headroom) minus that: one per
+  // head, the same in every lane; softmax sum of this lane's keys
+  float m_ref[NT][2], d_ref[NT][2], l_run[NT][2];
   int piece = -1, units = 0;
   for (int slot = 0;; ++slot) {
     const int s = slot % C::kStages;
@@ -725,8 +728,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         sl[nt][1] = qscale[nt * 8 + 2 * tig + 1];
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
-          n_ref[nt][f] = m_ref[nt][f] = kNoMax;
-          l_run[nt][f] = 0.f;
+          m_ref[nt][f] = kNoMax;
+          d_ref[nt][f] = l_run[nt][f] = 0.f;
         }
         if constexpr (!C::kQInSmem) {
 #pragma unroll
@@ -789,8 +792,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           }
         }
       // ---- softmax terms (no sink here) ----
-      // t = S * kscale; the softmax's exponent is t * sl - M, the numerator's t *
-      // sl + ev - m (n_ref is m - headroom): one FMA each.
+      // t = S * kscale; the softmax's exponent is t * sl - M, one FMA, the numerator's
+      // lies ev - (m - M) above it: m is held as its distance from M, so that logits
+      // too large for their difference of a few binades do not lose it.
       float t[KB][NT][4], ev[KB][2];
       const float down = *reinterpret_cast<const float *>(smem + q_off + C::kQScale + NT * 8 * 4);
 #pragma unroll
@@ -833,7 +837,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
 #pragma unroll
             for (int f = 0; f < 4; ++f) {
               zd[kb][nt][f] = fmaf(t[kb][nt][f], sl[nt][f & 1], -m_ref[nt][f & 1]);
-              zn[kb][nt][f] = fmaf(t[kb][nt][f], sl[nt][f & 1], ev[kb][f >> 1] - n_ref[nt][f & 1]);
+              zn[kb][nt][f] = zd[kb][nt][f] + (ev[kb][f >> 1] - d_ref[nt][f & 1]);
             }
       };
       exponents();
@@ -854,20 +858,26 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int f = 0; f < 2; ++f) {
-            float m1 = m_ref[nt][f], n1 = -INFINITY;
+            float m1 = -INFINITY, d1 = -INFINITY;
 #pragma unroll
-            for (int kb = 0; kb < KB; ++kb) {
-              const float x0 = t[kb][nt][f] * sl[nt][f], x1 = t[kb][nt][f + 2] * sl[nt][f];
-              m1 = fmaxf(m1, fmaxf(x0, x1));
-              n1 = fmaxf(n1, fmaxf(x0 + ev[kb][0], x1 + ev[kb][1]));
-            }
-            l_run[nt][f] *= ex2_approx(m_ref[nt][f] - m1);
+            for (int kb = 0; kb < KB; ++kb)
+              m1 = fmaxf(m1, fmaxf(t[kb][nt][f] * sl[nt][f], t[kb][nt][f + 2] * sl[nt][f]));
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, off));
+            m1 = fmaxf(m_ref[nt][f], m1);
+            const float fall = m_ref[nt][f] - m1;
+            l_run[nt][f] *= ex2_approx(fall);
             m_ref[nt][f] = m1;
 #pragma unroll
-            for (int off = 4; off < 32; off <<= 1) n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, off));
-            n1 = fmaxf(n_ref[nt][f], n1 - kHeadroom);
-            const float al = ex2_approx(n_ref[nt][f] - n1);
-            n_ref[nt][f] = n1;
+            for (int kb = 0; kb < KB; ++kb)
+              d1 = fmaxf(d1, fmaxf(fmaf(t[kb][nt][f], sl[nt][f], -m1) + ev[kb][0],
+                                   fmaf(t[kb][nt][f + 2], sl[nt][f], -m1) + ev[kb][1]));
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) d1 = fmaxf(d1, __shfl_xor_sync(0xffffffffu, d1, off));
+            const float d0 = d_ref[nt][f] + fall;
+            d1 = fmaxf(d0, d1 - kHeadroom);
+            const float al = ex2_approx(d0 - d1);
+            d_ref[nt][f] = d1;
 #pragma unroll
             for (int dm = 0; dm < D / 16; ++dm) {
               o[dm][nt][f] *= al;
@@ -945,14 +955,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
-        float M = m_ref[nt][f];
 #pragma unroll
-        for (int off = 4; off < 32; off <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-        float L = l_run[nt][f] * ex2_approx(m_ref[nt][f] - M);
-#pragma unroll
-        for (int off = 4; off < 32; off <<= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
-        m_ref[nt][f] = M;
-        l_run[nt][f] = L;
+        for (int off = 4; off < 32; off <<= 1) l_run[nt][f] += __shfl_xor_sync(0xffffffffu, l_run[nt][f], off);
       }
     // every warp is done with this stage
     __syncwarp();
@@ -971,7 +975,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
           const int at = warp * 8 + 2 * tig + f;
-          merge_n[at] = n_ref[nt][f];
+          merge_d[at] = d_ref[nt][f];
           merge_m[at] = m_ref[nt][f];
           merge_l[at] = l_run[nt][f];
         }

@@ -75,6 +75,46 @@ def test_keys_and_queries_of_opposite_sizes(form, key, query, scale):
     _check(c, FULL, D ** -0.5 if scale is None else scale, max(seqlens))
 
 
+def test_ordinary_heads_beside_extreme_ones():
+    """One group's heads of queries from 2^-124 to 2^15 (logits of 2^21, which single out a key) over ordinary keys."""
+    seqlens, MP, P, Hkv, G, D = [500, 70, 193], 8, 64, 1, 8, 128
+    c = list(_decode_case(35, seqlens, MP, P, Hkv, G, D, FULL))
+    rng = np.random.default_rng(36)
+    q = rng.standard_normal(c[0].shape) * 2.0 ** np.array([-124, -63, -23, -3, -2, -1, 14, 15])[None, :, None]
+    c[0] = torch.from_numpy(q).bfloat16()
+    ref, mag, top = cache8.decode(inputs.bits(c[0]), *c[1:], FULL, D ** -0.5)
+    got = _decode(*c, FULL, D ** -0.5)
+    assert np.isfinite(got).all() and top[:, 7].max() > 2.0 ** 20
+    assert (np.abs(got - ref) <= _tol(ref, mag, top, 500, D))[:, :6].all()
+
+
+@pytest.mark.parametrize("sink", [False, True])
+@pytest.mark.parametrize("at", [3, 62, -2])
+@pytest.mark.parametrize("form", FORMS)
+def test_one_key_far_above_the_others(form, at, sink):
+    """One key's logit is 2^9 .. 2^25 (in powers of two), the others' at most a seventh of it:
+    the output is that key's value row.  Exactly: the weight's rounding, 2^-11, is less than
+    half a bf16 step, and a row of codes needs no more than four of bf16's eight bits."""
+    seqlens, MP, P, Hkv, G, D = FORMS[form]
+    c = list(_decode_case(38, seqlens, MP, P, Hkv, G, D, FULL))
+    rng = np.random.default_rng(39)
+    c[4] = np.where(c[4] == 255, 255, rng.integers(120, 134, c[4].shape)).astype(np.uint8)
+    c[3] = np.where(c[3] == 255, 255, 127).astype(np.uint8)
+    c[1] = np.where(c[1] == 0x7F, c[1], (c[1] & 0x80) | np.minimum(c[1] & 0x7F, 0x5F)).astype(np.uint8)   # |k| <= 60
+    if not sink:
+        c[7][:] = -np.inf
+    sign = rng.integers(0, 2, (Hkv, D))
+    t = at % seqlens[0]
+    page, pos = int(c[5][0, t // P]), t % P
+    c[1][page, pos] = 0x7E | (sign << 7).astype(np.uint8)                                                 # |k| = 448
+    want = cache8.E4M3[c[2][page, pos]] * cache8.scales(c[4][page, :, pos])[:, None]
+    dirs = np.repeat(1.0 - 2.0 * sign, G, 0)
+    for log in range(9, 26):
+        c[0][0] = torch.from_numpy(dirs * 2.0 ** log * np.log(2) / 448 / D).bfloat16()
+        got = _decode(*c, FULL, 1.0)[0]
+        np.testing.assert_array_equal(got, np.repeat(want, G, 0), err_msg=str(log))
+
+
 def test_rows_read_back_at_the_ends_of_the_range_are_the_values_decoded():
     """Appended rows near bf16's ends, read back and decoded with one key visible: the
     decode gives that key's values exactly (no sink)."""
