@@ -30,6 +30,11 @@
  *    Argument errors are detected on the host before anything is launched; a
  *    one-line description of the last error on the calling thread is available
  *    from attn_sink_last_error().
+ *  - attn_sink_fwd_extend and the 8-bit cache's calls are launched with programmatic
+ *    dependence (in stream order all the same), and their short forms let the next
+ *    kernel come up while they run.  A kernel of the caller's that is itself
+ *    launched with that attribute waits (griddepcontrol.wait) before it reads
+ *    anything that earlier work of the stream writes, not only what the call writes.
  *  - Device-side waits are bounded.  A wait that runs out records
  *    ATTN_ETIMEOUT in a device status word and the kernel returns early;
  *    attn_sink_get_status() reads and clears that word.

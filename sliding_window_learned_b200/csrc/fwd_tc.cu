@@ -406,13 +406,6 @@ __global__ void __launch_bounds__(Cfg<D, BN, NH>::kThreads, Cfg<D, BN, NH>::kCta
     if (threadIdx.x == 0) report_launch_error(p.status, kWhereAlign);
     return;
   }
-  // (a grid on at most half the SMs, with no merge behind it: the next kernel may come
-  // up at once.  Three queries after 30 keys 6.6 -> 5.8 us a call; with more SMs taken
-  // its CTAs crowd where this one's end first: 30 single queries, 120 CTAs, 18.9 ->
-  // 19.9 us, 4 windowed chunks 57 -> 59)
-  if constexpr (kPrior) {
-    if (p.early) asm volatile("griddepcontrol.launch_dependents;");
-  }
   uint8_t *smem = smem_raw;
   uint8_t *sQ = smem;                       // [2] units' Q tiles, later their O staging
   uint8_t *sRing = smem + C::kQBytes;
@@ -525,6 +518,16 @@ __global__ void __launch_bounds__(Cfg<D, BN, NH>::kThreads, Cfg<D, BN, NH>::kCta
     named_barrier_sync(kBarTmem, C::kTmemThreads);
     tc_fence_after();
     tmem = *tmem_slot;
+    // A grid on at most half the SMs, with no merge behind it: the next kernel may come
+    // up from here on.  Only the warps behind the barrier say so: a CTA counts once it
+    // holds its columns, so that no kernel that comes up and waits for this one can
+    // take them from under an allocation that has yet to be served.  Three queries
+    // after 30 keys 6.8 -> 6.1 us a call; with more SMs taken its CTAs crowd where this
+    // one's end first: 30 single queries, 120 CTAs, 18.9 -> 19.9 us, 4 windowed chunks
+    // 57 -> 59.
+    if constexpr (kPrior) {
+      if (p.early) asm volatile("griddepcontrol.launch_dependents;");
+    }
   }
   // (kPrior is launched with programmatic dependence: what may overlap the kernel
   // before it ends here.  8 short chunks after up to 300 keys: 9.4 us, 10.5 without)
