@@ -167,8 +167,10 @@ int attn_sink_fwd_varlen(const attn_tensor *q, const attn_tensor *k, const attn_
  * LSE = its sink.  Rows of q outside every sequence are left as they are in out
  * and lse.  A NaN or infinity in a value row can reach queries of its own
  * sequence that do not see it (never another sequence's).
- * The softmax's weights go into the product with V as bf16 (as two bf16 terms where
- * T * Hq <= 512: few roundings do not average).
+ * The softmax's weights go into the product with V as bf16, as in the other
+ * forwards, but as two bf16 terms (2^-16 off instead of 2^-8) where T * Hq <= 512,
+ * where that costs least.  So a row may round differently beside other rows;
+ * attn_sink_fwd_extend_terms takes the choice from the size.
  * Supported head dims D: 64, 128, 256.  B = 0, T = 0 or max_seqlen_q = 0 is a
  * no-op.  Runs on the tcgen05/TMEM tensor-core kernel of attn_sink_fwd.
  */
@@ -176,6 +178,15 @@ int attn_sink_fwd_extend(const attn_tensor *q, const attn_tensor *k, const attn_
                          const attn_tensor *cu_seqlens_q, const attn_tensor *cu_seqlens_k,
                          int32_t max_seqlen_q, const attn_tensor *sinks, int32_t window, float scale,
                          attn_tensor *out, attn_tensor *lse, void *stream);
+
+/*
+ * attn_sink_fwd_extend with an explicit number of bf16 terms for the softmax's
+ * weights: 1, 2, or 0 for attn_sink_fwd_extend's own rule.
+ */
+int attn_sink_fwd_extend_terms(const attn_tensor *q, const attn_tensor *k, const attn_tensor *v,
+                               const attn_tensor *cu_seqlens_q, const attn_tensor *cu_seqlens_k,
+                               int32_t max_seqlen_q, const attn_tensor *sinks, int32_t window, float scale,
+                               int32_t terms, attn_tensor *out, attn_tensor *lse, void *stream);
 
 /*
  * The same operation on a plain CUDA-core fp32 kernel (one warp per output

@@ -42,7 +42,7 @@ _DTYPES = {torch.bfloat16: ATTN_DTYPE_BF16, torch.float32: ATTN_DTYPE_F32,
 EXPORTS = ("attn_sink_fwd", "attn_sink_fwd_max_logit", "attn_sink_fwd_varlen", "attn_sink_bwd", "attn_sink_fwd_cudacore", "attn_sink_decode",
            "attn_sink_decode_chunked", "attn_sink_decode_paged", "attn_sink_decode_fp8",
            "attn_sink_decode_noalloc",
-           "attn_sink_fwd_extend", "attn_sink_cache_append_fp8", "attn_sink_cache_read_fp8", "attn_sink_decode_paged_fp8",
+           "attn_sink_fwd_extend", "attn_sink_fwd_extend_terms", "attn_sink_cache_append_fp8", "attn_sink_cache_read_fp8", "attn_sink_decode_paged_fp8",
            "attn_sink_get_status", "attn_sink_set_wait_limit_ns", "attn_sink_fail_workspace_allocs",
            "attn_sink_strerror", "attn_sink_last_error")
 
@@ -98,6 +98,8 @@ def load() -> ctypes.CDLL:
             fn.restype = ctypes.c_int
         lib.attn_sink_fwd_extend.argtypes = [P, P, P, P, P, i32, P, i32, f32, P, P, V]
         lib.attn_sink_fwd_extend.restype = ctypes.c_int
+        lib.attn_sink_fwd_extend_terms.argtypes = [P, P, P, P, P, i32, P, i32, f32, i32, P, P, V]
+        lib.attn_sink_fwd_extend_terms.restype = ctypes.c_int
         lib.attn_sink_decode_paged_fp8.argtypes = [P] * 8 + [i32, f32, P, V]
         lib.attn_sink_decode_paged_fp8.restype = ctypes.c_int
         lib.attn_sink_get_status.argtypes = [V]
@@ -341,6 +343,16 @@ def attn_sink_fwd_extend(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int,
                                             window, scale, out, lse)
     if rc:
         _check(rc, "attn_sink_fwd_extend")
+
+
+def attn_sink_fwd_extend_terms(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int, sinks, window: int,
+                               scale: float, terms: int, out, lse=None, stream=None):
+    """C ``attn_sink_fwd_extend_terms``: attn_sink_fwd_extend with the softmax's
+    weights as ``terms`` bf16 terms (1 or 2; 0: by the number of rows)."""
+    rc = (_native or _binding()).fwd_extend_terms(_raw(stream), q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
+                                                  sinks, window, scale, terms, out, lse)
+    if rc:
+        _check(rc, "attn_sink_fwd_extend_terms")
 
 
 def attn_sink_set_wait_limit_ns(ns: int):

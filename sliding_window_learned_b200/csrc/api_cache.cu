@@ -111,6 +111,98 @@ int cache_call(const attn_tensor *k, const attn_tensor *v, const attn_tensor *kp
   return e == cudaSuccess ? ATTN_OK : fail_cuda(e, name);
 }
 
+int extend_call(const attn_tensor *q, const attn_tensor *k, const attn_tensor *v, const attn_tensor *cu_seqlens_q,
+                const attn_tensor *cu_seqlens_k, int32_t max_seqlen_q, const attn_tensor *sinks, int32_t window,
+                float scale, int32_t terms, attn_tensor *out, attn_tensor *lse, void *stream) {
+  int rc;
+  if ((rc = check_tensor(q, "q", ATTN_DTYPE_BF16, 3, true))) return rc;
+  if ((rc = check_tensor(k, "k", ATTN_DTYPE_BF16, 3, true))) return rc;
+  if ((rc = check_tensor(v, "v", ATTN_DTYPE_BF16, 3, true))) return rc;
+  if ((rc = check_tensor(cu_seqlens_q, "cu_seqlens_q", ATTN_DTYPE_I32, 1, false))) return rc;
+  if ((rc = check_tensor(cu_seqlens_k, "cu_seqlens_k", ATTN_DTYPE_I32, 1, false))) return rc;
+  if ((rc = check_tensor(sinks, "sinks", ATTN_DTYPE_F32, 1, false))) return rc;
+  if ((rc = check_tensor(out, "out", ATTN_DTYPE_BF16, 3, true))) return rc;
+  const int64_t T = q->shape[0], Hq = q->shape[1], D = q->shape[2], Tk = k->shape[0], Hkv = k->shape[1];
+  if (k->shape[2] != D) return fail(ATTN_EINVAL, "k head dim does not match q");
+  for (int d = 0; d < 3; ++d) {
+    if (v->shape[d] != k->shape[d]) return fail(ATTN_EINVAL, "v shape does not match k");
+    if (out->shape[d] != q->shape[d]) return fail(ATTN_EINVAL, "out shape does not match q");
+  }
+  const int64_t B = cu_seqlens_q->shape[0] - 1;
+  if (B < 0 || cu_seqlens_k->shape[0] != B + 1)
+    return fail(ATTN_EINVAL, "cu_seqlens_q and cu_seqlens_k need B + 1 >= 1 entries each");
+  if (B > 0 && (cu_seqlens_q->stride[0] != 1 || cu_seqlens_k->stride[0] != 1))
+    return fail(ATTN_EINVAL, "cu_seqlens_q and cu_seqlens_k must be contiguous");
+  if (sinks->shape[0] != Hq) return fail(ATTN_EINVAL, "sinks must have Hq = %lld entries", (long long)Hq);
+  if (Hq > 1 && sinks->stride[0] != 1) return fail(ATTN_EINVAL, "sinks must be contiguous");
+  if (Hq <= 0 || Hkv <= 0 || Hq % Hkv) return fail(ATTN_EINVAL, "Hq must be a positive multiple of Hkv");
+  if (window < 1) return fail(ATTN_EINVAL, "window must be >= 1");
+  if (max_seqlen_q < 0) return fail(ATTN_EINVAL, "max_seqlen_q must be >= 0");
+  if (!finite_pos(scale)) return fail(ATTN_EINVAL, "scale must be finite and > 0");
+  if (terms < 0 || terms > 2) return fail(ATTN_EINVAL, "terms must be 0, 1 or 2");
+  if (lse) {
+    if ((rc = check_tensor(lse, "lse", ATTN_DTYPE_F32, 2, false))) return rc;
+    if (lse->shape[0] != Hq || lse->shape[1] != T) return fail(ATTN_EINVAL, "lse must be [Hq, T]");
+  }
+  if (D != 64 && D != 128 && D != 256)
+    return fail(ATTN_EUNSUPPORTED, "head dim %lld not supported (64, 128, 256)", (long long)D);
+  if (B > 65535 || Hq > 65535 || T > (1LL << 30) || Tk > (1LL << 30))
+    return fail(ATTN_EUNSUPPORTED, "B and Hq must be <= 65535, T and Tk <= 2^30");
+  // no chunk is longer than T
+  const int64_t rows = max_seqlen_q < T ? max_seqlen_q : T;
+  // query tiles hold at least 112 rows (position, head) each, but for a sequence's last
+  if ((rows * Hq / 112 + Hq) * B > 0x7FFFFFFF)
+    return fail(ATTN_EUNSUPPORTED, "(max_seqlen_q / 112 + 1) * Hq * B must be < 2^31");
+  if (B == 0 || rows == 0) return ATTN_OK;
+  FwdArgs a;
+  a.q = q->data;
+  a.k = k->data;
+  a.v = v->data;
+  a.sinks = static_cast<const float *>(sinks->data);
+  a.out = out->data;
+  a.lse = lse ? static_cast<float *>(lse->data) : nullptr;
+  a.B = static_cast<int>(B);
+  a.L = static_cast<int>(rows);
+  a.T = static_cast<int>(T);
+  a.Tk = static_cast<int>(Tk);
+  a.Hq = static_cast<int>(Hq);
+  a.Hkv = static_cast<int>(Hkv);
+  a.D = static_cast<int>(D);
+  a.W = window < (1 << 30) ? window : (1 << 30);   // (positions are at least -2^30: no overflow)
+  a.scale = scale;
+  a.terms = terms;
+  a.cu_seqlens = static_cast<const int *>(cu_seqlens_q->data);
+  a.cu_seqlens_k = static_cast<const int *>(cu_seqlens_k->data);
+  // one batch slice of rows each: its (unused) batch stride spans the slice
+  const attn_tensor *ts[4] = {q, k, v, out};
+  int64_t *ss[4] = {a.q_s, a.k_s, a.v_s, a.o_s};
+  for (int x = 0; x < 4; ++x) {
+    ss[x][0] = (ts[x]->shape[0] > 0 ? ts[x]->shape[0] : 1) * ts[x]->stride[0];
+    ss[x][1] = ts[x]->stride[0];
+    ss[x][2] = ts[x]->stride[1];
+  }
+  a.lse_s[0] = 0;
+  a.lse_s[1] = lse ? lse->stride[0] : 0;
+  if ((rc = status_ptr(&a.status))) return rc;
+  if ((rc = sm_count(&a.sms))) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const size_t bytes = fwd_extend_workspace_bytes(a);
+  if (bytes == 0) {
+    const cudaError_t e = launch_fwd_tc(a, st);
+    return e == cudaSuccess ? ATTN_OK : fail_cuda(e, "attn_sink_fwd_extend launch");
+  }
+  cudaMemPool_t pool;
+  if ((rc = workspace_pool(&pool))) return rc;
+  if (take_injected_alloc_failure()) return fail(ATTN_ENOMEM, "extend workspace allocation failed (injected)");
+  cudaError_t e = cudaMallocFromPoolAsync(&a.workspace, bytes, pool, st);
+  if (e != cudaSuccess) return fail_cuda(e, "extend workspace allocation");
+  e = launch_fwd_tc(a, st);
+  const cudaError_t ef = cudaFreeAsync(a.workspace, st);
+  if (e != cudaSuccess) return fail_cuda(e, "attn_sink_fwd_extend launch");
+  if (ef != cudaSuccess) return fail_cuda(ef, "extend workspace release");
+  return ATTN_OK;
+}
+
 }  // namespace
 }  // namespace attnsink
 
@@ -216,91 +308,15 @@ int attn_sink_fwd_extend(const attn_tensor *q, const attn_tensor *k, const attn_
                          const attn_tensor *sinks, int32_t window, float scale, attn_tensor *out, attn_tensor *lse,
                          void *stream) {
   clear_error();
-  int rc;
-  if ((rc = check_tensor(q, "q", ATTN_DTYPE_BF16, 3, true))) return rc;
-  if ((rc = check_tensor(k, "k", ATTN_DTYPE_BF16, 3, true))) return rc;
-  if ((rc = check_tensor(v, "v", ATTN_DTYPE_BF16, 3, true))) return rc;
-  if ((rc = check_tensor(cu_seqlens_q, "cu_seqlens_q", ATTN_DTYPE_I32, 1, false))) return rc;
-  if ((rc = check_tensor(cu_seqlens_k, "cu_seqlens_k", ATTN_DTYPE_I32, 1, false))) return rc;
-  if ((rc = check_tensor(sinks, "sinks", ATTN_DTYPE_F32, 1, false))) return rc;
-  if ((rc = check_tensor(out, "out", ATTN_DTYPE_BF16, 3, true))) return rc;
-  const int64_t T = q->shape[0], Hq = q->shape[1], D = q->shape[2], Tk = k->shape[0], Hkv = k->shape[1];
-  if (k->shape[2] != D) return fail(ATTN_EINVAL, "k head dim does not match q");
-  for (int d = 0; d < 3; ++d) {
-    if (v->shape[d] != k->shape[d]) return fail(ATTN_EINVAL, "v shape does not match k");
-    if (out->shape[d] != q->shape[d]) return fail(ATTN_EINVAL, "out shape does not match q");
-  }
-  const int64_t B = cu_seqlens_q->shape[0] - 1;
-  if (B < 0 || cu_seqlens_k->shape[0] != B + 1)
-    return fail(ATTN_EINVAL, "cu_seqlens_q and cu_seqlens_k need B + 1 >= 1 entries each");
-  if (B > 0 && (cu_seqlens_q->stride[0] != 1 || cu_seqlens_k->stride[0] != 1))
-    return fail(ATTN_EINVAL, "cu_seqlens_q and cu_seqlens_k must be contiguous");
-  if (sinks->shape[0] != Hq) return fail(ATTN_EINVAL, "sinks must have Hq = %lld entries", (long long)Hq);
-  if (Hq > 1 && sinks->stride[0] != 1) return fail(ATTN_EINVAL, "sinks must be contiguous");
-  if (Hq <= 0 || Hkv <= 0 || Hq % Hkv) return fail(ATTN_EINVAL, "Hq must be a positive multiple of Hkv");
-  if (window < 1) return fail(ATTN_EINVAL, "window must be >= 1");
-  if (max_seqlen_q < 0) return fail(ATTN_EINVAL, "max_seqlen_q must be >= 0");
-  if (!finite_pos(scale)) return fail(ATTN_EINVAL, "scale must be finite and > 0");
-  if (lse) {
-    if ((rc = check_tensor(lse, "lse", ATTN_DTYPE_F32, 2, false))) return rc;
-    if (lse->shape[0] != Hq || lse->shape[1] != T) return fail(ATTN_EINVAL, "lse must be [Hq, T]");
-  }
-  if (D != 64 && D != 128 && D != 256)
-    return fail(ATTN_EUNSUPPORTED, "head dim %lld not supported (64, 128, 256)", (long long)D);
-  if (B > 65535 || Hq > 65535 || T > (1LL << 30) || Tk > (1LL << 30))
-    return fail(ATTN_EUNSUPPORTED, "B and Hq must be <= 65535, T and Tk <= 2^30");
-  // no chunk is longer than T
-  const int64_t rows = max_seqlen_q < T ? max_seqlen_q : T;
-  // query tiles hold at least 112 rows (position, head) each, but for a sequence's last
-  if ((rows * Hq / 112 + Hq) * B > 0x7FFFFFFF)
-    return fail(ATTN_EUNSUPPORTED, "(max_seqlen_q / 112 + 1) * Hq * B must be < 2^31");
-  if (B == 0 || rows == 0) return ATTN_OK;
-  FwdArgs a;
-  a.q = q->data;
-  a.k = k->data;
-  a.v = v->data;
-  a.sinks = static_cast<const float *>(sinks->data);
-  a.out = out->data;
-  a.lse = lse ? static_cast<float *>(lse->data) : nullptr;
-  a.B = static_cast<int>(B);
-  a.L = static_cast<int>(rows);
-  a.T = static_cast<int>(T);
-  a.Tk = static_cast<int>(Tk);
-  a.Hq = static_cast<int>(Hq);
-  a.Hkv = static_cast<int>(Hkv);
-  a.D = static_cast<int>(D);
-  a.W = window < (1 << 30) ? window : (1 << 30);   // (positions are at least -2^30: no overflow)
-  a.scale = scale;
-  a.cu_seqlens = static_cast<const int *>(cu_seqlens_q->data);
-  a.cu_seqlens_k = static_cast<const int *>(cu_seqlens_k->data);
-  // one batch slice of rows each: its (unused) batch stride spans the slice
-  const attn_tensor *ts[4] = {q, k, v, out};
-  int64_t *ss[4] = {a.q_s, a.k_s, a.v_s, a.o_s};
-  for (int x = 0; x < 4; ++x) {
-    ss[x][0] = (ts[x]->shape[0] > 0 ? ts[x]->shape[0] : 1) * ts[x]->stride[0];
-    ss[x][1] = ts[x]->stride[0];
-    ss[x][2] = ts[x]->stride[1];
-  }
-  a.lse_s[0] = 0;
-  a.lse_s[1] = lse ? lse->stride[0] : 0;
-  if ((rc = status_ptr(&a.status))) return rc;
-  if ((rc = sm_count(&a.sms))) return rc;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const size_t bytes = fwd_extend_workspace_bytes(a);
-  if (bytes == 0) {
-    const cudaError_t e = launch_fwd_tc(a, st);
-    return e == cudaSuccess ? ATTN_OK : fail_cuda(e, "attn_sink_fwd_extend launch");
-  }
-  cudaMemPool_t pool;
-  if ((rc = workspace_pool(&pool))) return rc;
-  if (take_injected_alloc_failure()) return fail(ATTN_ENOMEM, "extend workspace allocation failed (injected)");
-  cudaError_t e = cudaMallocFromPoolAsync(&a.workspace, bytes, pool, st);
-  if (e != cudaSuccess) return fail_cuda(e, "extend workspace allocation");
-  e = launch_fwd_tc(a, st);
-  const cudaError_t ef = cudaFreeAsync(a.workspace, st);
-  if (e != cudaSuccess) return fail_cuda(e, "attn_sink_fwd_extend launch");
-  if (ef != cudaSuccess) return fail_cuda(ef, "extend workspace release");
-  return ATTN_OK;
+  return extend_call(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, sinks, window, scale, 0, out, lse, stream);
+}
+
+int attn_sink_fwd_extend_terms(const attn_tensor *q, const attn_tensor *k, const attn_tensor *v,
+                               const attn_tensor *cu_seqlens_q, const attn_tensor *cu_seqlens_k,
+                               int32_t max_seqlen_q, const attn_tensor *sinks, int32_t window, float scale,
+                               int32_t terms, attn_tensor *out, attn_tensor *lse, void *stream) {
+  clear_error();
+  return extend_call(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, sinks, window, scale, terms, out, lse, stream);
 }
 
 }  // extern "C"

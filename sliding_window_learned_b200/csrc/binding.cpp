@@ -194,6 +194,23 @@ PyObject *fwd_extend(PyObject *, PyObject *const *a, Py_ssize_t n) {
   });
 }
 
+// (stream, q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, sinks, window, scale, terms, out, lse or None)
+PyObject *fwd_extend_terms(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject * {
+    static constexpr int at[8] = {1, 2, 3, 4, 5, 7, 11, 12};
+    Call c;
+    int32_t max_q, window, terms;
+    float scale;
+    if (!count(n, 13) || !tensors(a, at, 8, 1u << 7, &c) || !as_int32(a[6], &max_q) || !as_int32(a[8], &window) ||
+        !as_float(a[9], &scale) || !as_int32(a[10], &terms))
+      return nullptr;
+    return run(c, [&] {
+      return attn_sink_fwd_extend_terms(c.p[0], c.p[1], c.p[2], c.p[3], c.p[4], max_q, c.p[5], window, scale, terms,
+                                        c.p[6], c.p[7], c.stream);
+    });
+  });
+}
+
 // (METH_FASTCALL functions have a signature of their own)
 PyCFunction fast(PyObject *(*f)(PyObject *, PyObject *const *, Py_ssize_t)) {
   return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f));
@@ -204,6 +221,7 @@ PyMethodDef methods[] = {
     {"cache_read", fast(cache_read), METH_FASTCALL, nullptr},
     {"decode_paged", fast(decode_paged), METH_FASTCALL, nullptr},
     {"fwd_extend", fast(fwd_extend), METH_FASTCALL, nullptr},
+    {"fwd_extend_terms", fast(fwd_extend_terms), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -1028,12 +1028,16 @@ int prior_splits(const FwdArgs &a, int ctas_per_sm, int sms) {
 
 // Whether P goes into a kPrior product as two bf16 terms, 2^-16 of it off instead of
 // 2^-8.  One term's error is about that of the bf16 output (together 1.4 times the
-// output's own); over many rows it averages to that, but a call of few rows can have
-// 1.6 times.  Such calls wait for memory and launches, and two terms cost them 5..12 %
-// (3 queries of 12 heads after 1 K keys 14.5 -> 15.7 us); a call that fills the
-// machine would pay 13..29 % (4096 queries after 12 K keys 960 -> 1235 us).
+// output's own, up to 1.6 over a call of few rows), two leave the output's own.  A
+// row's error does not depend on the rows beside it, the price does: calls of few rows
+// wait for memory and launches, and the second term costs them 5..12 % (3 queries of
+// 12 heads after 1 K keys 14.5 -> 15.7 us); a call that fills the machine pays 13..29 %
+// (4096 queries after 12 K keys 960 -> 1235 us).  So unless the caller says, the
+// number of rows decides.
 constexpr int kTwoTermRows = 512;
-bool prior_two_terms(const FwdArgs &a) { return static_cast<int64_t>(a.T) * a.Hq <= kTwoTermRows; }
+bool prior_two_terms(const FwdArgs &a) {
+  return a.terms == 0 ? static_cast<int64_t>(a.T) * a.Hq <= kTwoTermRows : a.terms == 2;
+}
 
 template <int D, int BN, int NH, bool kPacked, bool kMaxLogit = false, bool kPrior = false, bool kTwo = false>
 cudaError_t launch(const FwdArgs &a, cudaStream_t stream) {

@@ -33,6 +33,7 @@ struct FwdArgs {
   const int *cu_seqlens_k = nullptr;
   int Tk = 0;
   int sms = 0;                             // (with cu_seqlens_k) multiprocessors
+  int terms = 0;                           // (with cu_seqlens_k) bf16 terms of the softmax's weights; 0: by size
   void *workspace = nullptr;               // fwd_extend_workspace_bytes, or null if that is 0
   // Largest content logit per (batch, query head): [B, Hq] f32 (row stride
   // ml_sb), batched inputs only; null: not computed.
