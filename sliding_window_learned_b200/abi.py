@@ -291,6 +291,10 @@ def _binding():
         except ImportError as e:
             raise ImportError(f"_binding.so is not built ({e}); run "
                               "`python -m sliding_window_learned_b200.build`") from e
+        from .build import binding_for
+        if native.built_for != binding_for():
+            raise ImportError(f"_binding.so was built for {native.built_for}, this is {binding_for()}; run "
+                              "`python -m sliding_window_learned_b200.build`")
         _native = native
     return _native
 
