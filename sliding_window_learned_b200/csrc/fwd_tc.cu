@@ -138,13 +138,18 @@ struct Params {
   float *o_part, *lse_part;
 };
 
-// A kPrior unit: query tile, head group, sequence and its share of the key tiles.
-struct PriorUnit {
+// A work unit: query tile, head group and sequence.  The sequence has `len` positions
+// from row `row0` of the row dimension and `klen` keys from row `krow0`; the tile's
+// first row m0 is at position pm0 and takes n_tiles key tiles from kt0 (with packed
+// sequences a unit past its sequence's end is empty, n_tiles = 0, and every role
+// skips it).
+struct Unit {
   int m0, h0, b, row0, len, krow0, klen, pm0, kt0, n_tiles;
 };
+// A kPrior unit: its share of the key tiles too.
 template <int BN>
-__device__ __forceinline__ PriorUnit prior_unit(const Params &p, int u) {
-  PriorUnit t;
+__device__ __forceinline__ Unit prior_unit(const Params &p, int u) {
+  Unit t;
   const int sp = u % p.nsplit, x = u / p.nsplit;
   const int groups = p.Hq / p.pack, per_m = groups * p.B;
   const int mt = p.num_m_tiles - 1 - x / per_m;
@@ -430,33 +435,12 @@ __global__ void __launch_bounds__(Cfg<D, BN, NH>::kThreads, Cfg<D, BN, NH>::kCta
   // Work units: (query tile, head group, batch), latest query tiles first (they
   // see the most keys under a causal window), head groups fastest so that the
   // CTAs running at the same time share K/V tiles in L2.  CTA c takes units
-  // c, c + gridDim.x, ...
-  // A unit's sequence has `len` positions starting at row `row0` of the
-  // row dimension, in batch slice bc() of the tensor maps; with packed
-  // sequences a unit past its sequence's end is empty (n_tiles = 0) and every
-  // role skips it.
-  struct Unit {
-    int m0, h0, b, kt0, n_tiles, len, row0;
-    int pm0, klen, krow0;                  // position of row m0; the keys' count and first row
-  };
+  // c, c + gridDim.x, ..., each in batch slice bc() of the tensor maps.
   constexpr bool packed = kPacked;
   auto bc = [&](const Unit &t) { return packed ? 0 : t.b; };
   auto unit_at = [&](int u) {
+    if constexpr (kPrior) return prior_unit<BN>(p, u);
     Unit t;
-    if constexpr (kPrior) {
-      const PriorUnit x = prior_unit<BN>(p, u);
-      t.m0 = x.m0;
-      t.h0 = x.h0;
-      t.b = x.b;
-      t.kt0 = x.kt0;
-      t.n_tiles = x.n_tiles;
-      t.len = x.len;
-      t.row0 = x.row0;
-      t.pm0 = x.pm0;
-      t.klen = x.klen;
-      t.krow0 = x.krow0;
-      return t;
-    }
     const int per_m = HP * p.B;
     const int mt = p.num_m_tiles - 1 - u / per_m;
     const int r = u - (u / per_m) * per_m;
@@ -542,19 +526,6 @@ __global__ void __launch_bounds__(Cfg<D, BN, NH>::kThreads, Cfg<D, BN, NH>::kCta
       tma_prefetch_desc(&tmV);
       int slot = 0, q_loaded = 0;
       bool ok = true;
-      auto load = [&](const CUtensorMap *map, int kt, int b) {
-        const int s = slot % C::kStages;
-        const uint32_t use = static_cast<uint32_t>(slot / C::kStages);
-        if (slot >= C::kStages && !mbar_wait(&empty[s], (use & 1u) ^ 1u, ctx, kWhereEmpty)) {
-          ok = false;
-          return;
-        }
-        mbar_arrive_expect_tx(&full[s], C::kTileBytes);
-        uint8_t *dst = sRing + s * C::kTileBytes;
-        for (int c = 0; c < C::kChunks; ++c)
-          tma_load_4d(dst + c * BN * 128, map, &full[s], c * 64, 0, kt * BN, b);
-        ++slot;
-      };
       int ul = -1;                            // units that are not empty, so far
       for (int u = blockIdx.x; ok && u < p.num_units; u += gridDim.x) {
         const Unit t = unit_at(u);
@@ -597,7 +568,6 @@ __global__ void __launch_bounds__(Cfg<D, BN, NH>::kThreads, Cfg<D, BN, NH>::kCta
           if (ok && j + C::kSBuf < t.n_tiles) kv(&tmK, t.kt0 + j + C::kSBuf);
         }
       }
-      (void)load;
       // Before this warp leaves, the copies it issued have landed: the CTA (and
       // its shared memory) must outlive them even when the other roles gave
       // up early.  Only the last two Q loads and the last kStages K/V tiles
@@ -945,7 +915,7 @@ __global__ void __launch_bounds__(kCombineRows * 32) prior_combine_kernel(const 
   constexpr int kPer = D / 32;                     // channels per lane, consecutive
   const int lane = threadIdx.x & 31, r = blockIdx.y * kCombineRows + (threadIdx.x >> 5);
   const int u0 = blockIdx.x * p.nsplit;
-  const PriorUnit t = prior_unit<BN>(p, u0 + min(lane, p.nsplit - 1));   // (lane s: split s)
+  const Unit t = prior_unit<BN>(p, u0 + min(lane, p.nsplit - 1));   // (lane s: split s)
   const int i = t.m0 + r / p.pack, h = t.h0 + r % p.pack;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (r >= p.ppt * p.pack || i >= t.len) return;
