@@ -27,7 +27,8 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 // Blocks of the one wave, per SM.  Measured at 8 x 16 K rows, 8 kv heads, D = 128
 // (4 / 3 / 2): append 122 / 127 / 152 us, read 146 / 143 / 126 us: the read's
-// writes, two thirds of its bytes, do better from fewer places at a time.  A read
+// writes, two thirds of its bytes, do better from fewer places at a time.  (Short
+// replays; back to back, under the power cap, append 139 and read 129 us.)  A read
 // of few iterations is bound by latency instead and takes four (47 K rows of 2
 // heads, D = 64: 9.5 us, 10.9 with two).
 constexpr int kAppendBlocks = 4, kReadBlocks = 2, kShortReadBlocks = 4;

@@ -41,11 +41,12 @@
 //              states at the end of a piece while the consumers go on.
 //
 // Bound by HBM at long contexts: D + 1 bytes per key, kv head and K or V.  64
-// sequences of 4 K..131 K keys, Hq32 Hkv4 D128, 256-position pages: 640 us, 7.2
-// TB/s (1.10 of the measured copy rate, which reads and writes); 8 of them 108 us,
-// 6.2 TB/s, where the start (2 us to the first copies, then every CTA's first
-// stages at once) and the end show.  With 16 heads a group the consumers' chain of
-// dependent instructions bounds it: 5.6 TB/s.  Tried and dropped, each against the
+// sequences of 4 K..131 K keys, Hq32 Hkv4 D128, 256-position pages, calls back to
+// back: 774 us, 6.0 TB/s (0.91 of the measured copy rate), with the clock at 1.5 GHz
+// under the power cap; 640 us in short replays at 1.9 GHz, as all figures from here
+// on.  8 of them 109 us (118 back to back), where the start (2 us to the first
+// copies, then every CTA's first stages at once) and the end show.  With 16 heads a
+// group the consumers' chain of dependent instructions bounds it: 5.6 TB/s.  Tried and dropped, each against the
 // version it was tried on: K's codes straight into e4m3 MMAs with q as two e4m3
 // terms (a quarter fewer instructions, but those MMAs' latency is longer: 643 ->
 // 720 us, 16 heads 503 -> 667); the consumers as two groups that take tiles in turn
@@ -564,19 +565,20 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             float M = kNoMax;
 #pragma unroll
             for (int w = 0; w < C::kCW; ++w) M = fmaxf(M, merge_m[w * 8 + hl]);
-            float N = kNoMax;              // the numerator's reference, less M
-#pragma unroll
-            for (int w = 0; w < C::kCW; ++w) N = fmaxf(N, merge_m[w * 8 + hl] - M + merge_d[w * 8 + hl]);
-            // the numerator on its own largest reference: 2^N joins only behind the
-            // division, so that neither the sum of large values nor the weights of small
-            // ones leave f32 where their mean does not
-            float den = 0.f;
-            float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+            float N = kNoMax, den = 0.f;   // the numerator's reference, less M
 #pragma unroll
             for (int w = 0; w < C::kCW; ++w) {
               const float below = merge_m[w * 8 + hl] - M;
+              N = fmaxf(N, below + merge_d[w * 8 + hl]);
               den += merge_l[w * 8 + hl] * ex2_approx(below);
-              const float f = ex2_approx(below + merge_d[w * 8 + hl] - N);
+            }
+            // the numerator on its own largest reference: 2^N joins only behind the
+            // division, so that neither the sum of large values nor the weights of small
+            // ones leave f32 where their mean does not
+            float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < C::kCW; ++w) {
+              const float f = ex2_approx(merge_m[w * 8 + hl] - M + merge_d[w * 8 + hl] - N);
               const float4 v = *reinterpret_cast<const float4 *>(mbuf + (w * 8 + hl) * D + (d ^ (hl >> 1 << 3)));
               num.x = fmaf(f, v.x, num.x);
               num.y = fmaf(f, v.y, num.y);
