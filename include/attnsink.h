@@ -166,7 +166,9 @@ int attn_sink_fwd_varlen(const attn_tensor *q, const attn_tensor *k, const attn_
  * passed: the W - 1 before the chunk.  A query with p < 0 sees none: O = 0 and
  * LSE = its sink.  Rows of q outside every sequence are left as they are in out
  * and lse.  A NaN or infinity in a value row can reach queries of its own
- * sequence that do not see it (never another sequence's).
+ * sequence that do not see it (never another sequence's).  Weighted values are summed
+ * before the division, with weights up to 2^8: values beyond 2^119 / (keys seen) may
+ * overflow, as in the other forwards.
  * The softmax's weights go into the product with V as bf16, as in the other
  * forwards, but as two bf16 terms (2^-16 off instead of 2^-8) where T * Hq <= 512,
  * where that costs least.  So a row may round differently beside other rows;
