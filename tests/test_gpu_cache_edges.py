@@ -164,3 +164,74 @@ def test_decode_widest_window_of_whole_and_cut():
     for seqlens, MP in (([500, 70], 8), ([1400, 0, 900], 24)):
         c = _decode_case(98, seqlens, MP, 64, 2, 4, 128, FULL)
         np.testing.assert_array_equal(_decode(*c, WIDEST, 0.1), _decode(*c, FULL, 0.1))
+
+
+def test_rows_whose_offsets_pass_32_bits():
+    """k and v of 2.3e9 elements (4.7 GB): appended, and read back, at both ends."""
+    T, Hkv, D, P = 1150003, 8, 256, 64
+    pages = -(-T // P)
+    e4, e8 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+    z = lambda *s: torch.zeros(*s, dtype=torch.uint8, device=DEV)  # noqa: E731
+    pools = (z(pages, P, Hkv, D).view(e4), z(pages, P, Hkv, D).view(e4), z(pages, Hkv, P).view(e8), z(pages, Hkv, P).view(e8))
+    table, sl, cu = torch.arange(pages - 1, -1, -1, dtype=torch.int32, device=DEV)[None], _i32([T]), _i32([0, T])
+    k, v = (torch.zeros(T, Hkv, D, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    assert k.numel() > 1 << 31
+    rng = np.random.default_rng(99)
+    ends = [slice(0, 300), slice(T // 2, T // 2 + 300), slice(T - 300, T)]
+    rows = [(_rows(rng, 300, Hkv, D), _rows(rng, 300, Hkv, D)) for _ in ends]
+    for e, (a, b) in zip(ends, rows):
+        k[e], v[e] = a.to(DEV), b.to(DEV)
+    swl.attn_sink_cache_append_fp8(k, v, table, sl, cu, *pools)
+    k.fill_(7), v.fill_(7)
+    swl.attn_sink_cache_read_fp8(*pools, table, sl, cu, k, v)
+    for e, ab in zip(ends, rows):
+        for got, x in zip((k, v), ab):
+            codes, scale = cache8.quantise(inputs.bits(x))
+            np.testing.assert_array_equal(got[e].double().cpu().numpy(), cache8.E4M3[codes] * cache8.scales(scale)[..., None])
+    between = torch.ones(T, dtype=torch.bool, device=DEV)
+    for e in ends:
+        between[e] = False
+    at = between.nonzero()[:: 97, 0]
+    assert not k[at].any() and not v[at].any()
+    assert swl.attn_sink_get_status() == 0
+
+
+def test_queries_whose_offsets_pass_32_bits():
+    """q and out of 2.3e9 elements, each query beside its own key alone (W = 1)."""
+    T, Hq, D = 70001, 128, 256
+    g = torch.Generator(device=DEV).manual_seed(100)
+    q = torch.zeros(T, Hq, D, dtype=torch.bfloat16, device=DEV)
+    k, v = (torch.randn(T, 4, D, generator=g, device=DEV).bfloat16() for _ in range(2))
+    assert q.numel() > 1 << 31
+    ends = (0, T // 2, T - 50)
+    for e in ends:
+        q[e: e + 50] = torch.randn(50, Hq, D, generator=g, device=DEV).bfloat16()
+    sinks = torch.linspace(-2, 3, Hq, device=DEV)
+    out, lse = torch.empty_like(q), torch.empty(Hq, T, device=DEV)
+    cu = _i32([0, T])
+    swl.attn_sink_fwd_extend(q, k, v, cu, cu, T, sinks, 1, 0.1, out, lse)
+    torch.cuda.synchronize()
+    assert swl.attn_sink_get_status() == 0
+    for e in ends:
+        x = [t[e: e + 50] for t in (q, k, v)]
+        one = np.array([0, 50])
+        ro, rl, mag, top = cache8.extend(*(inputs.bits(t.cpu()) for t in x), one, one, sinks.cpu().numpy(), 1, 0.1)
+        assert (np.abs(out[e: e + 50].double().cpu().numpy() - ro) <= _tol_extend(ro, mag, top, 1, D)).all()
+        assert (np.abs(lse[:, e: e + 50].double().cpu().numpy() - rl) <= _tol_lse(rl, top, 1, D)).all()
+
+
+@pytest.mark.parametrize("terms", [1, 2])
+def test_a_captured_call_of_either_number_of_terms(terms):
+    q, k, v, cu_q, cu_k, sinks = _case(101, [5, 40], [2500, 1900], 2, 8, 128, tail=(0, 0))
+    args = (q.to(DEV), k.to(DEV), v.to(DEV), _i32(cu_q), _i32(cu_k), 40, torch.from_numpy(sinks).to(DEV), FULL, 0.1, terms)
+    want, got = torch.empty_like(q, device=DEV), torch.zeros_like(q, device=DEV)
+    swl.attn_sink_fwd_extend_terms(*args, want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        swl.attn_sink_fwd_extend_terms(*args, got)
+    for _ in range(3):
+        got.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+    assert swl.attn_sink_get_status() == 0
